@@ -13,7 +13,8 @@ LIB_PATH = os.path.join(HERE, "libpw.so")
 PW_OK, PW_ERR_INVALID_ARG, PW_ERR_UNSUPPORTED, PW_ERR_BAD_SELECTION, PW_ERR_CAPACITY, \
     PW_ERR_TIMEOUT, PW_ERR_CUDA = range(7)
 
-EXPORTED = ("pw_version", "pw_status_string", "pw_groups_size", "pw_group", "pw_attn")
+EXPORTED = ("pw_version", "pw_status_string", "pw_groups_size", "pw_group", "pw_attn",
+            "pw_qk_norm_rope", "pw_append", "pw_chunk_workspace_size", "pw_chunk_attn")
 
 
 class PwGroups(C.Structure):
@@ -65,6 +66,18 @@ def load() -> C.CDLL:
     L.pw_attn.argtypes = [p, p, p, p, C.c_int, C.c_int, p, C.c_int, i64, C.c_int, C.c_int,
                           f32, f32, f32, C.POINTER(PwGroups), p, p, p]
     L.pw_attn.restype = C.c_int
+    i = C.c_int
+    L.pw_qk_norm_rope.argtypes = [p, i64, i64, i, p, i64, i64, i, p, i, p, i, f32, p, i, i, i, p, p,
+                                  i, i64, p, i64, i64, p, i64, i64, p, p]
+    L.pw_qk_norm_rope.restype = i
+    L.pw_append.argtypes = [p, i64, i64, p, i64, i64, i, p, i, f32, p, i, i, i, p, p, i, i64, p, i, i,
+                            f32, f32, p, p, p, p]
+    L.pw_append.restype = i
+    L.pw_chunk_workspace_size.argtypes = [i, i64, i, i, i, C.POINTER(sz)]
+    L.pw_chunk_workspace_size.restype = i
+    L.pw_chunk_attn.argtypes = [p, i64, i64, i, p, p, i, p, i, i, p, p, i, i64, i, i, f32, f32, f32,
+                                p, p, p, sz, p, p]
+    L.pw_chunk_attn.restype = i
     _lib = L
     return L
 

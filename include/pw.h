@@ -174,6 +174,97 @@ pw_status pw_group_noalloc(const int32_t *sel_pages, const int32_t *cu_seqlens,
                            const int32_t *cu_seqlens_host, int B, int Hkv, int kmax, int W, int g,
                            const pw_groups *groups, int32_t *dev_status, void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * New tokens over the paged cache: query/key preparation, append, dense attention.
+ *
+ * The sparse prefill above reads K_pages / V_pages; the three calls below write that cache and
+ * attend over all of it, for a ragged batch of new tokens (a prompt, a chunk of one, drafted
+ * tokens, or one token per sequence).  The paper has no counterpart: they are what a serving
+ * loop runs around the sparse prefill.  One step is pw_qk_norm_rope (queries), pw_append (keys
+ * and values), pw_chunk_attn, on one stream; with ctx_lens = 0 the pages pw_append writes are
+ * also what pw_attn reads.
+ *
+ * Shared by the three calls
+ *   cu_seqlens  int32 [B+1]  offsets of the NEW tokens of each sequence among the T rows;
+ *                            cu[0] = 0, non-decreasing
+ *   ctx_lens    int32 [B]    tokens of each sequence that are in the cache already; NULL = 0.
+ *                            Token i of sequence b has position ctx_lens[b] + i.
+ *   T           rows that the caller's buffers hold.  Rows from cu_seqlens[B] on (a padded
+ *               batch) are neither read nor written.
+ * The lengths are read on the device only, so a captured graph may be replayed after they
+ * change.  Nothing here resets *dev_status: the first error is recorded and stays.
+ * Rows of heads: element (t, h, d) of a [T, H, 128] argument is at t * stride_t + h * stride_h + d.
+ * Strides count elements and are multiples of 8; data starts on a 16-byte boundary.  An output's
+ * rows must not overlap.
+ */
+
+/* Norm and rotation of query and key heads in one pass.
+ * Per row x of 128:  y = x / sqrt(mean(x^2) + eps) * weight  (weight NULL: y = x), then the first
+ * rot_dim elements are rotated by the angle a(p, i) of the token's position p: pairs
+ * (y[i], y[i + rot_dim / 2]), or with interleaved (y[2i], y[2i + 1]), become
+ * (u cos a - v sin a, u sin a + v cos a).  fp32 throughout, rounded to bf16 once.
+ *   Q, K            bf16 rows of heads (K may be NULL with Hk = 0; Q with Hq = 0)
+ *   q_weight, ...   bf16 [128] (weight_stride 0: one weight for all heads) or [H, 128]
+ *                   (weight_stride 128), 16-byte aligned; NULL = no norm of those heads
+ *   rope            fp32 [max_pos, rot_dim]: cos a(p, 0..rot_dim/2-1), then sin; 16-byte aligned.
+ *                   NULL or rot_dim 0 = no rotation.  rot_dim is a multiple of 16, at most 128.
+ *   Q_out, K_out    bf16 rows of heads; the same buffer and strides as the input, or no overlap
+ *                   with any input
+ * A position outside [0, max_pos) records PW_ERR_INVALID_ARG; its rows are not rotated. */
+pw_status pw_qk_norm_rope(const void *Q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
+                          const void *K, int64_t k_stride_t, int64_t k_stride_h, int Hk,
+                          const void *q_weight, int q_weight_stride, const void *k_weight,
+                          int k_weight_stride, float eps, const float *rope, int max_pos,
+                          int rot_dim, int interleaved, const int32_t *cu_seqlens,
+                          const int32_t *ctx_lens, int B, int64_t T, void *Q_out,
+                          int64_t qo_stride_t, int64_t qo_stride_h, void *K_out,
+                          int64_t ko_stride_t, int64_t ko_stride_h, int32_t *dev_status,
+                          void *stream);
+
+/* Keys and values of the new tokens into the paged cache, with the keys' norm and rotation (as in
+ * pw_qk_norm_rope) on the way.  The codes are E4M3 of key / k_scale and value / v_scale, rounded
+ * to nearest even; magnitudes above 448 become 448, NaN stays NaN.  The row of position p goes to
+ * slot p % 64 of physical page page_table[b * max_pages + p / 64]; nothing else of the cache is
+ * written.  Two tokens of one call must not share a slot.
+ *   K, V              bf16 rows of heads, Hkv heads each
+ *   K_pages, V_pages  uint8 [n_phys, Hkv, 64, 128], 16-byte aligned
+ * Scales are positive and finite.  A position whose page lies outside the table's row, or whose
+ * table entry is outside [0, n_phys), records PW_ERR_INVALID_ARG and is not written; so does a
+ * position outside [0, max_pos) of the rotation's table. */
+pw_status pw_append(const void *K, int64_t k_stride_t, int64_t k_stride_h, const void *V,
+                    int64_t v_stride_t, int64_t v_stride_h, int Hkv, const void *k_weight,
+                    int k_weight_stride, float eps, const float *rope, int max_pos, int rot_dim,
+                    int interleaved, const int32_t *cu_seqlens, const int32_t *ctx_lens, int B,
+                    int64_t T, const int32_t *page_table, int max_pages, int n_phys,
+                    float k_scale, float v_scale, void *K_pages, void *V_pages,
+                    int32_t *dev_status, void *stream);
+
+/* Device scratch pw_chunk_attn needs for these shapes (256-byte aligned start), computed on the
+ * host.  It grows with neither T nor the context lengths. */
+pw_status pw_chunk_workspace_size(int B, int64_t T, int Hq, int Hkv, int max_q_len,
+                                  size_t *workspace_bytes);
+
+/* Attention of the new tokens over the paged cache (which holds their own keys and values too).
+ * Token at position p attends to the keys at positions p - window + 1 .. p (window 0: 0 .. p):
+ *   O[t, hq, :] = v_scale * softmax(sm_scale * k_scale * q K^T) V, rounded to bf16, and, where lse
+ * is given, lse[t * Hq + hq] = log sum_j exp(sm_scale * k_scale * q k_j).
+ *   Q               bf16 rows of heads (Hq of them); query head hq uses kv head hq / (Hq / Hkv)
+ *   O               bf16 [T, Hq, 128], contiguous
+ *   max_q_len       longest chunk of the batch, on the host.  It chooses the kernel; the results
+ *                   are right for any positive value.
+ *   workspace       pw_chunk_workspace_size bytes for the same B, T, Hq, Hkv and max_q_len; calls
+ *                   that overlap in time must not share it.  It needs no clearing.
+ * Supported: Hq % Hkv == 0, positions below 2^30.  sm_scale is positive and finite, scales too.
+ * A page-table entry outside [0, n_phys), or a position outside the table's row, records
+ * PW_ERR_INVALID_ARG and nothing is read outside the cache. */
+pw_status pw_chunk_attn(const void *Q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
+                        const void *K_pages, const void *V_pages, int Hkv,
+                        const int32_t *page_table, int max_pages, int n_phys,
+                        const int32_t *cu_seqlens, const int32_t *ctx_lens, int B, int64_t T,
+                        int max_q_len, int window, float k_scale, float v_scale, float sm_scale,
+                        void *O, float *lse, void *workspace, size_t workspace_bytes,
+                        int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
