@@ -7,8 +7,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "pw_attn_common.cuh"
-#include "pw_tokens.cuh"
+#include "pw_chunk.cuh"
 
 namespace pw {
 namespace {
@@ -108,10 +107,64 @@ __global__ void __launch_bounds__(256) k_chunk_rows(const ChunkLaunch L)
 
 } // namespace
 
-size_t chunk_workspace(int, int64_t, int, int, int) { return 256; }
+namespace chunk {
+
+namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once through the runtime (no link to libcuda).
+EncodeTiledFn encode_tiled()
+{
+    static const EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+} // namespace
+
+cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap *map)
+{
+    const EncodeTiledFn enc = encode_tiled();
+    if (enc == nullptr)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(L.pm.n_phys) * L.Hkv * kPageTokens};
+    const cuuint64_t strides[1] = {kHeadDim};
+    const cuuint32_t box[2] = {kHeadDim, kPageTokens}, ones[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(pages), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+} // namespace chunk
+
+size_t chunk_workspace(int, int64_t, int Hq, int Hkv, int max_q_len)
+{
+    return chunk::decode_workspace(static_cast<int>(min(static_cast<int64_t>(max_q_len) * (Hq / Hkv), static_cast<int64_t>(1) << 20)));
+}
 
 cudaError_t chunk_launch(const ChunkLaunch &L, cudaStream_t st)
 {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t rows = static_cast<int64_t>(L.max_q_len) * L.G;
+    if (rows <= 64)
+        return chunk::decode_launch(L, static_cast<int>(rows), min(sms, chunk::kMaxCtas), st);
     k_chunk_rows<<<static_cast<unsigned>((L.tb.T * L.Hq + 7) / 8), 256, 0, st>>>(L);
     return cudaGetLastError();
 }

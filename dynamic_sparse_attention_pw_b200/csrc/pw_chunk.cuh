@@ -1,0 +1,503 @@
+// pw_chunk.cuh -- what the two kernels of pw_chunk_attn share: how the work is cut into tiles and
+// dealt out to the CTAs, the partial results of tiles that several CTAs work on, bounded waits.
+//
+// Work.  The rows of a sequence and kv head are its tokens times the G query heads that share the
+// kv head, flat index token * G + head.  A tile is NT consecutive rows; its keys (the union of what
+// its rows see) are cut into blocks of 128 positions, two pages.  All blocks of all tiles form one
+// line, ordered by (sequence, kv head, tile, block), and the CTAs take equal stretches of it, so
+// one long context, many short ones and any mixture fill the GPU alike.  The lengths are read
+// on the device, by every CTA for itself (a block scan over the sequences).
+//
+// A tile that lies within one stretch is finished by its CTA.  One that is cut leaves partial
+// results (fp32 accumulator, running maximum, sum) in the workspace, at most two of a CTA: the end
+// of a tile that an earlier CTA began (slot 0) and the beginning of one that goes on (slot 1).
+// k_chunk_merge joins them in CTA order, so the result does not depend on timing.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pw_attn_common.cuh"
+#include "pw_tokens.cuh"
+
+namespace pw {
+namespace chunk {
+
+using namespace tokens;
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kMaxCtas = 148;  // one CTA per SM
+constexpr int kBlock = 128;    // keys per block
+constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
+
+struct Sequence {
+    int row0;     // first row of Q (token) of the sequence
+    int qlen;     // new tokens
+    int64_t ctx;  // tokens before them
+    int64_t last; // last position the page table's row can hold
+};
+
+// Contents that the arguments rule out (offsets outside [0, T] or falling, a negative context, a
+// position outside the table's row) are recorded and clamped, so that nothing is addressed outside
+// the caller's buffers.
+__device__ __forceinline__ Sequence sequence(const ChunkLaunch &L, int b)
+{
+    Sequence s;
+    const int T = static_cast<int>(L.tb.T);
+    const int c0 = __ldg(L.tb.cu + b), c1 = __ldg(L.tb.cu + b + 1);
+    const int ctx = L.tb.ctx != nullptr ? __ldg(L.tb.ctx + b) : 0;
+    s.row0 = min(max(c0, 0), T);
+    s.qlen = max(min(max(c1, 0), T) - s.row0, 0);
+    s.ctx = max(ctx, 0);
+    s.last = static_cast<int64_t>(L.pm.max_pages) * kPageTokens - 1;
+    if (c0 != s.row0 || c1 != s.row0 + s.qlen || (s.qlen > 0 && (ctx < 0 || s.ctx + s.qlen - 1 > s.last)))
+        set_status(L.status, PW_ERR_INVALID_ARG);
+    return s;
+}
+
+struct Tile {
+    int row, rows;  // flat rows of the sequence and kv head
+    int lo, hi;     // keys [lo, hi) that some row of it sees
+    int blk0, nblk; // their blocks
+};
+
+__device__ __forceinline__ int position(const Sequence &s, int token)
+{
+    return static_cast<int>(min(s.ctx + token, s.last));
+}
+
+template <int NT>
+__device__ __forceinline__ Tile tile_of(const ChunkLaunch &L, const Sequence &s, int i)
+{
+    Tile t;
+    t.row = i * NT;
+    t.rows = min(s.qlen * L.G - t.row, NT);
+    t.hi = position(s, (t.row + t.rows - 1) / L.G) + 1;
+    t.lo = L.window > 0 ? max(position(s, t.row / L.G) - L.window + 1, 0) : 0;
+    t.blk0 = t.lo / kBlock;
+    t.nblk = (t.hi + kBlock - 1) / kBlock - t.blk0;
+    return t;
+}
+
+template <int NT>
+__device__ __forceinline__ int tiles_of(const ChunkLaunch &L, const Sequence &s)
+{
+    return (s.qlen * L.G + NT - 1) / NT;
+}
+
+// Blocks of one kv head of sequence b.
+template <int NT>
+__device__ __forceinline__ int64_t head_blocks(const ChunkLaunch &L, int b)
+{
+    const Sequence s = sequence(L, b);
+    int64_t n = 0;
+    for (int i = 0, e = tiles_of<NT>(L, s); i < e; ++i)
+        n += tile_of<NT>(L, s, i).nblk;
+    return n;
+}
+
+struct Plan {
+    int64_t total;   // blocks of the whole call
+    int64_t x0, x1;  // this CTA's stretch
+    int64_t b_start; // first block of sequence b0
+    int64_t per_head; // blocks of one kv head of sequence b0
+    int b0;          // sequence that x0 lies in
+    int ctas;        // CTAs with work
+    int64_t scan[33];
+};
+
+__device__ __forceinline__ int64_t stretch(int64_t total, int ctas, int j) { return total * j / ctas; }
+
+// Block-wide inclusive scan of v; returns it and the sum in `sum`.  scratch: 33 words.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64_t &sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(kFull, v, d);
+        if (lane >= d)
+            v += o;
+    }
+    __syncthreads();
+    if (lane == 31)
+        scratch[warp] = v;
+    __syncthreads();
+    int64_t before = 0;
+    sum = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i < warp)
+            before += scratch[i];
+        sum += scratch[i];
+    }
+    return v + before;
+}
+
+// Every thread of the CTA calls it; the plan is in shared memory afterwards.  min_blocks: a CTA is
+// given at least that many blocks.
+template <int NT>
+__device__ void make_plan(const ChunkLaunch &L, Plan &p, int cta, int min_blocks)
+{
+    const int nt = blockDim.x, tid = threadIdx.x, B = L.tb.B;
+    int64_t mine = tid < B ? head_blocks<NT>(L, tid) : 0, total = 0;
+    int64_t all = mine;
+    for (int b = tid + nt; b < B; b += nt)
+        all += head_blocks<NT>(L, b);
+    (void)block_scan(all, p.scan, total);
+    total *= L.Hkv;
+    const int ctas = static_cast<int>(max(min(static_cast<int64_t>(gridDim.x), total / min_blocks), static_cast<int64_t>(1)));
+    const int64_t x0 = cta < ctas ? stretch(total, ctas, cta) : total;
+    const int64_t x1 = cta < ctas ? stretch(total, ctas, cta + 1) : total;
+    if (tid == 0) {
+        p.total = total;
+        p.x0 = x0;
+        p.x1 = x1;
+        p.ctas = ctas;
+        p.b0 = 0;
+        p.b_start = 0;
+        p.per_head = 1;
+    }
+    int64_t run = 0;
+    if (x0 < x1) { // uniform
+        for (int base = 0; base < B; base += nt) {
+            const int b = base + tid;
+            if (base > 0)
+                mine = b < B ? head_blocks<NT>(L, b) : 0;
+            int64_t sum;
+            const int64_t incl = run + block_scan(mine, p.scan, sum) * L.Hkv;
+            if (mine > 0 && incl - mine * L.Hkv <= x0 && x0 < incl) {
+                p.b0 = b;
+                p.b_start = incl - mine * L.Hkv;
+                p.per_head = mine;
+            }
+            run += sum * L.Hkv;
+            if (run > x0)
+                break;
+        }
+    }
+    __syncthreads();
+}
+
+// One piece of a tile, as the roles of a CTA hand it on.
+struct Job {
+    int nblk;      // blocks of the piece; -1: no more
+    int blk0;      // first of them
+    int lo, hi;    // the tile's keys
+    int row, rows; // the tile's rows
+    int b, h;
+    int tok0;      // Q row of the sequence's first token
+    int slot;      // -1: the whole tile, 0 / 1: partial
+};
+
+// Where the tile that stretch j starts in was cut, for k_chunk_merge.
+struct Cut {
+    int64_t total, ts, te; // all blocks; first block of the tile and the one behind its last
+    int ctas, inside;      // inside: the stretch starts behind the tile's first block
+    int row, rows, h, tok0;
+};
+
+template <int NT>
+__host__ __device__ constexpr size_t partial_floats() { return static_cast<size_t>(NT) * (kHeadDim + 2); }
+
+constexpr size_t kCutBytes = (sizeof(Cut) * kMaxCtas + 255) / 256 * 256;
+
+template <int NT>
+__host__ __device__ constexpr size_t workspace_bytes() { return kCutBytes + 2 * kMaxCtas * partial_floats<NT>() * sizeof(float); }
+
+// Partial of CTA j, slot s: acc [NT][128], then max [NT], then sum [NT].
+template <int NT>
+__device__ __forceinline__ float *partial(const ChunkLaunch &L, int j, int s)
+{
+    return reinterpret_cast<float *>(static_cast<uint8_t *>(L.workspace) + kCutBytes) +
+           (static_cast<size_t>(j) * 2 + s) * partial_floats<NT>();
+}
+
+// The pieces of a CTA's stretch, one after the other; a warp runs it (uniformly).
+template <int NT>
+struct Pieces {
+    int64_t x, x1;
+    int b, h, i, off; // next piece: tile i of (b, h), from its block off on
+    Sequence s;
+    int tiles;
+
+    __device__ __forceinline__ void begin(const ChunkLaunch &L, const Plan &p, Cut *cuts, int cta, int lane)
+    {
+        x = p.x0;
+        x1 = p.x1;
+        if (x >= x1) {
+            if (lane == 0 && cta < kMaxCtas)
+                cuts[cta].inside = 0;
+            return;
+        }
+        b = p.b0;
+        s = sequence(L, b);
+        tiles = tiles_of<NT>(L, s);
+        int64_t rest = x - p.b_start;
+        h = static_cast<int>(rest / p.per_head);
+        rest -= h * p.per_head;
+        // 32 tiles at a time
+        for (i = 0;; i += 32) {
+            int n = i + lane < tiles ? tile_of<NT>(L, s, i + lane).nblk : 0;
+            int incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kFull, incl, d);
+                if (lane >= d)
+                    incl += o;
+            }
+            const uint32_t beyond = __ballot_sync(kFull, incl > rest);
+            if (beyond != 0u) {
+                const int k = __ffs(beyond) - 1;
+                i += k;
+                off = static_cast<int>(rest) - __shfl_sync(kFull, incl - n, k);
+                break;
+            }
+            const int sum = __shfl_sync(kFull, incl, 31);
+            if (sum == 0 && i + 32 >= tiles) { // cannot happen while the lengths stay as they were
+                x = x1;
+                if (lane == 0)
+                    cuts[cta].inside = 0;
+                return;
+            }
+            rest -= sum;
+        }
+        if (lane == 0) {
+            const Tile t = tile_of<NT>(L, s, i);
+            cuts[cta] = Cut{p.total, x - off, x - off + t.nblk, p.ctas, off > 0, t.row, t.rows, h, s.row0};
+        }
+    }
+
+    __device__ __forceinline__ bool next(const ChunkLaunch &L, Job &j)
+    {
+        if (x >= x1)
+            return false;
+        const Tile t = tile_of<NT>(L, s, i);
+        const int n = static_cast<int>(min(static_cast<int64_t>(t.nblk - off), x1 - x));
+        j = Job{n, t.blk0 + off, t.lo, t.hi, t.row, t.rows, b, h, s.row0, off > 0 ? 0 : (n < t.nblk ? 1 : -1)};
+        x += n;
+        off = 0;
+        if (++i == tiles) {
+            i = 0;
+            if (++h == L.Hkv) {
+                h = 0;
+                while (x < x1 && ++b < L.tb.B) {
+                    s = sequence(L, b);
+                    tiles = tiles_of<NT>(L, s);
+                    if (tiles > 0)
+                        break;
+                }
+                if (b >= L.tb.B)
+                    x = x1;
+            }
+        }
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------------------
+// Bounded waits: a CTA whose wait runs out raises its abort flag, which ends every other wait in it.
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+static __device__ __noinline__ bool wait_spin(uint64_t *bar, uint32_t parity, int32_t *abort_flag)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (*reinterpret_cast<volatile int32_t *>(abort_flag) != 0)
+            return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *reinterpret_cast<volatile int32_t *>(abort_flag) = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int32_t *abort_flag)
+{
+    return mbar_try_wait(bar, parity) || wait_spin(bar, parity, abort_flag);
+}
+
+// The whole warp waits and agrees.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *abort_flag)
+{
+    return __all_sync(kFull, wait_bar(bar, parity, abort_flag));
+}
+
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane)
+{
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(bar);
+}
+
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool pred)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 q, %1, 0;\n\t"
+                 "bar.red.or.pred p, %2, %3, q;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(r)
+                 : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// ---------------------------------------------------------------------------------------
+// Queries: a row times the power of two that brings its largest magnitude into [128, 256), split
+// into two E4M3 parts whose sum is exact for every element within 2^9 of the largest (a bf16 value
+// has 8 significant bits, a part 4).
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t max_exp8(const uint4 v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = max(m, max((w[i] >> 7) & 0xFFu, (w[i] >> 23) & 0xFFu));
+    return m;
+}
+
+__device__ __forceinline__ int q_exp(uint32_t e) { return min(max(134 - static_cast<int>(e), -126), 126); }
+__device__ __forceinline__ float exp2i(int s) { return __int_as_float((s + 127) << 23); }
+
+__device__ __forceinline__ void e4m3x2_to_f32(uint32_t pair, float &lo, float &hi)
+{
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(pair)));
+    const __half2 h = *reinterpret_cast<const __half2 *>(&h2);
+    lo = __low2float(h);
+    hi = __high2float(h);
+}
+
+__device__ __forceinline__ void split_q8(const uint4 v, float scale, uint2 &q1, uint2 &q2)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x0 = bf16_lo(w[i]) * scale, x1 = bf16_hi(w[i]) * scale;
+        a[i] = e4m3x2(x0, x1);
+        float y0, y1;
+        e4m3x2_to_f32(a[i], y0, y1);
+        b[i] = e4m3x2(x0 - y0, x1 - y1);
+    }
+    q1 = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16));
+    q2 = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+}
+
+// Sixteen lanes of a half-warp (l = lane % 16) bring one row: its two parts into rows r1 and r2 of a
+// K-major operand tile (128-byte rows, 128-byte swizzle).  Returns the factor that takes the parts'
+// score to a base-2 exponent; NaN for a row that holds an infinity or NaN, so that its output is NaN.
+// A null row stores zeros.
+__device__ __forceinline__ float stage_q_row(const uint16_t *row, uint8_t *tile, int r1, int r2, int l, float score_scale)
+{
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (row != nullptr)
+        v = __ldg(reinterpret_cast<const uint4 *>(row) + l);
+    uint32_t e = max_exp8(v);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1)
+        e = max(e, __shfl_xor_sync(kFull, e, d));
+    const int s = q_exp(e);
+    uint2 q1, q2;
+    split_q8(v, exp2i(s), q1, q2);
+    const int in = (l & 1) * 8;
+    *reinterpret_cast<uint2 *>(tile + attn::swz(r1, l >> 1) + in) = q1;
+    *reinterpret_cast<uint2 *>(tile + attn::swz(r2, l >> 1) + in) = q2;
+    // kept above zero, so that a masked score (-infinity) stays one in a row of zeros
+    return e == 255u ? __int_as_float(0x7FC00000) : fmaxf(score_scale * exp2i(-s), 1e-30f);
+}
+
+// Physical slot of a page, checked; 0 where the entry is bad (recorded).
+__device__ __forceinline__ int phys_slot(const ChunkLaunch &L, int b, int page)
+{
+    const int p = page < L.pm.max_pages ? __ldg(L.pm.table + static_cast<int64_t>(b) * L.pm.max_pages + page) : -1;
+    if (p < 0 || p >= L.pm.n_phys) {
+        set_status(L.status, PW_ERR_INVALID_ARG);
+        return 0;
+    }
+    return p;
+}
+
+// A cache as a 2-D byte tensor [n_phys * Hkv * 64][128] in boxes of one page with the 128-byte
+// swizzle, so that one copy lands a page as a matrix operand.
+cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap *map);
+
+cudaError_t decode_launch(const ChunkLaunch &L, int rows, int ctas, cudaStream_t st);
+size_t decode_workspace(int rows);
+
+// Joins the partial results of the tiles that were cut: the block of stretch j does the tile that
+// the stretch starts inside of, unless an earlier stretch starts inside of it too.  One warp per row.
+template <int NT>
+__global__ void __launch_bounds__(128) k_chunk_merge(const ChunkLaunch L)
+{
+    const int j = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const Cut c = reinterpret_cast<const Cut *>(L.workspace)[j];
+    if (!c.inside || r >= c.rows || stretch(c.total, c.ctas, j - 1) > c.ts)
+        return;
+    int n = 1; // pieces: slot 1 of CTA j - 1, slot 0 of CTAs j .. j + n - 2
+    while (j + n - 1 < c.ctas && stretch(c.total, c.ctas, j + n - 1) < c.te)
+        ++n;
+    const float *first = partial<NT>(L, j - 1, 1), *rest = partial<NT>(L, j, 0);
+    auto piece = [&](int i) { return i == 0 ? first : rest + static_cast<size_t>(i - 1) * 2 * partial_floats<NT>(); };
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        top = fmaxf(top, piece(i)[NT * kHeadDim + r]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < n) {
+            const float *p = piece(i0 + lane);
+            w = attn::ex2(p[NT * kHeadDim + r] - top);
+            sum += w * p[NT * (kHeadDim + 1) + r];
+        }
+        const int m = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
+            const float wi = __shfl_sync(kFull, w, i);
+            const float4 o = reinterpret_cast<const float4 *>(piece(i0 + i) + r * kHeadDim)[lane];
+            acc.x = fmaf(wi, o.x, acc.x);
+            acc.y = fmaf(wi, o.y, acc.y);
+            acc.z = fmaf(wi, o.z, acc.z);
+            acc.w = fmaf(wi, o.w, acc.w);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(kFull, sum, d);
+    const float inv = L.v_scale / sum;
+    const int flat = c.row + r, tok = flat / L.G;
+    const int64_t at = (static_cast<int64_t>(c.tok0) + tok) * L.Hq + c.h * L.G + flat - tok * L.G;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2 *>(L.O + at * kHeadDim)[lane] =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    if (L.lse != nullptr && lane == 0)
+        L.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int NT>
+cudaError_t merge_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
+{
+    k_chunk_merge<NT><<<dim3(ctas, (NT + 3) / 4), 128, 0, st>>>(L);
+    return cudaGetLastError();
+}
+
+} // namespace chunk
+} // namespace pw
