@@ -401,12 +401,9 @@ __device__ __forceinline__ void split_q8(const uint4 v, float scale, uint2 &q1, 
 // Sixteen lanes of a half-warp (l = lane % 16) bring one row: its two parts into rows r1 and r2 of a
 // K-major operand tile (128-byte rows, 128-byte swizzle).  Returns the factor that takes the parts'
 // score to a base-2 exponent; NaN for a row that holds an infinity or NaN, so that its output is NaN.
-// A null row stores zeros.
-__device__ __forceinline__ float stage_q_row(const uint16_t *row, uint8_t *tile, int r1, int r2, int l, float score_scale)
+// v: the lane's eight elements.
+__device__ __forceinline__ float stage_q_row(const uint4 v, uint8_t *tile, int r1, int r2, int l, float score_scale)
 {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row != nullptr)
-        v = __ldg(reinterpret_cast<const uint4 *>(row) + l);
     uint32_t e = max_exp8(v);
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1)

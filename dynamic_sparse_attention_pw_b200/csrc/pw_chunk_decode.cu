@@ -15,13 +15,18 @@
 // of it.  That costs one vote per block instead of a reduction over the keys, which lie along the
 // threads here.
 //
-// Two groups of four softmax warps take blocks in turn (block c goes to group c % 2), each with its
-// own S, P, accumulator, reference and sums; they meet at the end of a tile.
+// Two groups of eight softmax warps take blocks in turn (block c goes to group c % 2), each with its
+// own S, P, accumulator, reference and sums; they meet at the end of a tile.  The two warps of a
+// group that share a quarter of the keys share its rows: four of every eight each.  Sixteen warps
+// because the chain of a block is latency, not issue: with four warps a group it took 2600 cycles
+// for every eight rows.  Code that a tile runs once (its first block, its end) is kept short: at the
+// start of a call it runs from a cold instruction cache, and unrolled over the rows it alone took
+// 14 us.
 //
 //   warp 0       load: page ids, TMA copies into the ring of K and V stages, job records
 //   warp 1       the products
 //   warps 2-3    the next tile's queries
-//   warps 4-11   softmax (two groups), and the end of a tile
+//   warps 4-19   softmax (two groups), and the end of a tile
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -34,10 +39,14 @@ namespace pw {
 namespace chunk {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kSoftmax = 512;  // threads of the softmax warps
 constexpr int kJobs = 4;
+// Query tiles: S runs up to two blocks, so up to two tiles, ahead of the products, and a tile's slot is
+// free when its results are written.
+constexpr int kQ = 3;
 constexpr int kMinBlocks = 1;
-constexpr uint32_t kBarBoth = 3; // named barrier of the two softmax groups (theirs: 1 and 2)
+constexpr uint32_t kBarAll = 5; // named barrier of all softmax warps (the groups' halves: 1 to 4)
 constexpr float kRaise = 8.f; // a row's reference moves when a score exceeds it by more (base 2),
 constexpr float kBelow = 4.f; // to this much below that score
 
@@ -49,16 +58,17 @@ struct __align__(1024) DecSmem {
     uint8_t k[kStages][kBlock * 128]; // 128 keys x 128 dims
     uint8_t v[kStages][kBlock * 128];
     uint8_t p[2][3 * NT * 128];       // [group][part, row][key]
-    uint8_t q[2][2 * NT * 128];       // [tile % 2][part, row][dim]
-    float stage[NT][128];             // group 1's accumulator at the end of a tile
-    float2 cm[2][NT];                 // [group]: score factor and reference of a row
-    float red[2][4][NT];              // [group][warp]: block maxima, row sums
-    float c[2][NT];                   // [tile % 2]: score factor
-    int pos[2][NT];                   // [tile % 2]: position of the row's token
+    uint8_t q[kQ][2 * NT * 128];      // [tile % kQ][part, row][dim]
+    float c[kQ][NT];                  // [tile % kQ]: factor of a row's scores
+    int pos[kQ][NT];                  // [tile % kQ]: position of the row's token
+    int at[kQ][NT];                   // [tile % kQ]: its row of O and lse
+    float nm[2][NT];                  // [group]: a row's reference, negated
+    float alpha[2][NT];               // [group]: factor when it moves
+    float red[2][4][NT];              // [group][key quarter]: block maxima, row sums
     Job job[kJobs];
     Plan plan;
     uint64_t job_full[kJobs], job_empty[kJobs];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[kQ], q_empty[kQ];
     uint64_t k_full[kStages], v_full[kStages], st_empty[kStages];
     uint64_t s_done[2], s_free[2], p_ready[2], pv_done[2];
     uint64_t drain;
@@ -67,39 +77,86 @@ struct __align__(1024) DecSmem {
     int32_t abort_flag;
 };
 
-// One key's weights of two rows: three E4M3 parts each (byte 0: the first row's), the second and
-// third scaled by 2^4 and 2^8.
-__device__ __forceinline__ void split3(float p0, float p1, uint32_t &a, uint32_t &b, uint32_t &c)
+using F2 = uint64_t; // two fp32, for the packed instructions
+
+__device__ __forceinline__ F2 pack2(float lo, float hi)
 {
-    float y0, y1;
-    a = e4m3x2(p0, p1);
-    e4m3x2_to_f32(a, y0, y1);
-    p0 = (p0 - y0) * 16.f;
-    p1 = (p1 - y1) * 16.f;
-    b = e4m3x2(p0, p1);
-    e4m3x2_to_f32(b, y0, y1);
-    c = e4m3x2((p0 - y0) * 16.f, (p1 - y1) * 16.f);
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r)
+__device__ __forceinline__ void unpack2(F2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// One key's weights of two rows, rounded to f16 and split exactly into three E4M3 parts each (byte
+// 0: the first row's), the second and third times 2^4 and 2^8.
+__device__ __forceinline__ void split3(float p0, float p1, uint32_t (&w)[3])
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(p1), "f"(p0));
+    __half2 x = *reinterpret_cast<__half2 *>(&h);
+    const __half2 k16 = __float2half2_rn(16.f);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        uint16_t e;
+        uint32_t y;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<uint32_t *>(&x)));
+        w[i] = e;
+        if (i < 2) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(e));
+            x = __hmul2(__hsub2(x, *reinterpret_cast<__half2 *>(&y)), k16);
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_max(float x)
+{
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t (&r)[2])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 
 // Waits for this thread's tcgen05.ld; the registers pass through it, so that no use moves before.
-__device__ __forceinline__ void tmem_wait8(uint32_t *r)
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+    static_assert(N == 2 || N == 4, "");
+    if (N == 2)
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1])::"memory");
+    else
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[N - 2]), "+r"(r[N - 1])::"memory");
 }
 
 template <int NT>
@@ -119,15 +176,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kJobs; ++i) {
             mbar_init(&sm.job_full[i], 1);
-            mbar_init(&sm.job_empty[i], 2 + 1 + 8); // query, product and softmax warps
+            mbar_init(&sm.job_empty[i], 2 + 1 + 16); // query, product and softmax warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 2);
-            mbar_init(&sm.q_empty[i], 1 + 8); // products, softmax warps
             mbar_init(&sm.s_done[i], 1);
-            mbar_init(&sm.s_free[i], 4);
-            mbar_init(&sm.p_ready[i], 4);
+            mbar_init(&sm.s_free[i], 8);
+            mbar_init(&sm.p_ready[i], 8);
             mbar_init(&sm.pv_done[i], 1);
+        }
+        for (int i = 0; i < kQ; ++i) {
+            mbar_init(&sm.q_full[i], 2);
+            mbar_init(&sm.q_empty[i], 1 + 16); // products, softmax warps
         }
         for (int i = 0; i < kSt; ++i) {
             mbar_init(&sm.k_full[i], 1);
@@ -154,33 +213,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- load ----------------
         Pieces<NT> pieces;
         pieces.begin(L, sm.plan, reinterpret_cast<Cut *>(L.workspace), cta, lane);
+        // slots of the 32 pages of job j from block k on, one a lane
+        auto fetch = [&](const Job &j, int k) {
+            const int pg = 2 * (j.blk0 + k) + lane; // between the pages that hold a key of the tile
+            return pg >= (j.lo >> 6) && pg <= ((j.hi - 1) >> 6) && pg < 2 * (j.blk0 + j.nblk) ? phys_slot(L, j.b, pg) : -1;
+        };
         uint32_t c = 0;
-        bool ok = true;
+        Job j;
+        bool more = pieces.next(L, j), ok = true;
+        int ids = more ? fetch(j, 0) : -1;
         for (uint32_t n = 0; ok; ++n) {
-            Job j;
-            const bool more = pieces.next(L, j);
-            if (!more)
-                j.nblk = -1;
             ok = warp_wait(&sm.job_empty[n % kJobs], ((n / kJobs) & 1u) ^ 1u, ab);
             if (!ok)
                 break;
+            if (!more)
+                j.nblk = -1;
             if (lane == 0) {
                 sm.job[n % kJobs] = j;
                 mbar_arrive(&sm.job_full[n % kJobs]);
             }
             if (!more)
                 break;
-            const int plo = j.lo >> 6, phi = (j.hi - 1) >> 6; // pages that hold a key of the tile
-            const int p0 = 2 * j.blk0;
-            auto fetch = [&](int k) { // slots of the 32 pages from block k on, one a lane
-                const int pg = p0 + 2 * k + lane;
-                return pg >= plo && pg <= phi && pg < p0 + 2 * j.nblk ? phys_slot(L, j.b, pg) : -1;
-            };
-            int ids = fetch(0), nxt = fetch(16);
+            Job jn;
+            int ids_n = -1, nxt = j.nblk > 16 ? fetch(j, 16) : -1;
+            // the next job is formed, and its first page ids asked for, while copies are in flight
+            const int ahead = min(j.nblk, kSt) - 1;
             for (int k = 0; k < j.nblk; ++k, ++c) {
                 if (k > 0 && (k & 15) == 0) {
                     ids = nxt;
-                    nxt = fetch(k + 16);
+                    if (k + 16 < j.nblk)
+                        nxt = fetch(j, k + 16);
                 }
                 const int s0 = __shfl_sync(kFull, ids, 2 * (k & 15)), s1 = __shfl_sync(kFull, ids, 2 * (k & 15) + 1);
                 const uint32_t s = c % kSt;
@@ -203,12 +265,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sm.issued = c + 1;
                 }
                 __syncwarp();
+                if (k == ahead) {
+                    more = pieces.next(L, jn);
+                    if (more)
+                        ids_n = fetch(jn, 0);
+                }
             }
+            j = jn;
+            ids = ids_n;
         }
     } else if (warp == 1) {
         // ---------------- products ----------------
-        // S of block c goes out before the products of block c - 2, the last block of the same
-        // group: its S is read by then, so it computes while that group forms its weights.
+        // S of block c goes out before the products of block c - 2, the last block of the same group,
+        // also across the end of a tile: its S is read by then, so it computes while that group forms
+        // its weights.
         const uint64_t dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024), dv = sdesc_sw128(smem_u32(sm.v[0]), 16, 1024);
         const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dp = sdesc_sw128(smem_u32(sm.p[0]), 16, 1024);
         uint32_t c = 0;
@@ -230,20 +300,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return true;
         };
+        bool f1 = false, f2 = false; // blocks c - 1 and c - 2 are the first of their group in a tile
         for (uint32_t n = 0; ok; ++n) {
             ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
             if (!ok)
                 break;
             const int nblk = sm.job[n % kJobs].nblk;
             warp_arrive(&sm.job_empty[n % kJobs], lane);
-            if (nblk < 0)
-                break;
-            const uint32_t qb = n & 1u;
-            ok = warp_wait(&sm.q_full[qb], (n >> 1) & 1u, ab);
-            for (int k = 0; ok && k < nblk + 2; ++k) {
-                if (k < nblk) {
-                    const uint32_t cc = c + k, g = cc & 1u, s = cc % kSt;
-                    ok = warp_wait(&sm.k_full[s], (cc / kSt) & 1u, ab) && warp_wait(&sm.s_free[g], ((cc >> 1) & 1u) ^ 1u, ab);
+            const uint32_t qb = n % kQ;
+            if (nblk >= 0)
+                ok = warp_wait(&sm.q_full[qb], (n / kQ) & 1u, ab);
+            // behind the last job: the products that are left
+            for (int k = 0; ok && k < (nblk >= 0 ? nblk : 2); ++k, ++c) {
+                if (nblk >= 0) {
+                    const uint32_t g = c & 1u, s = c % kSt;
+                    ok = warp_wait(&sm.k_full[s], (c / kSt) & 1u, ab) && warp_wait(&sm.s_free[g], ((c >> 1) & 1u) ^ 1u, ab);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -258,10 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (k >= 2)
-                    ok = pv(c + k - 2, k < 4);
+                if (c >= 2)
+                    ok = pv(c - 2, f2);
+                f2 = f1;
+                f1 = k < 2;
             }
-            c += nblk;
+            if (nblk < 0)
+                break;
         }
     } else if (warp < 4) {
         // ---------------- queries ----------------
@@ -273,20 +347,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_arrive(&sm.job_empty[n % kJobs], lane);
             if (j.nblk < 0)
                 break;
-            const uint32_t qb = n & 1u;
-            if (!warp_wait(&sm.q_empty[qb], ((n >> 1) & 1u) ^ 1u, ab))
+            const uint32_t qb = n % kQ;
+            if (!warp_wait(&sm.q_empty[qb], ((n / kQ) & 1u) ^ 1u, ab))
                 break;
             const Sequence s = sequence(L, j.b);
-            for (int r = 2 * (warp - 2) + half; r < NT; r += 4) {
-                const int flat = j.row + r, tok = flat / L.G;
-                const bool real = r < j.rows;
-                const uint16_t *row = real ? L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
-                                                 static_cast<int64_t>(j.h * L.G + flat - tok * L.G) * L.q_sh
-                                           : nullptr;
-                const float c = stage_q_row(row, sm.q[qb], r, NT + r, l, L.score_scale);
-                if (l == 0) {
-                    sm.c[qb][r] = c;
-                    sm.pos[qb][r] = real ? position(s, tok) : -1;
+            // sixteen lanes a row, two rows of a half-warp at a time
+            for (int r0 = 2 * (warp - 2) + half; r0 < NT; r0 += 8) {
+                uint4 v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = r0 + 4 * i, flat = j.row + r, tok = flat / L.G, head = j.h * L.G + flat - tok * L.G;
+                    const bool real = r < j.rows;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (real)
+                        v[i] = __ldg(reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
+                                                                     static_cast<int64_t>(head) * L.q_sh) + l);
+                    if (l == 0) {
+                        sm.pos[qb][r] = real ? position(s, tok) : -1;
+                        sm.at[qb][r] = (j.tok0 + tok) * L.Hq + head;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = r0 + 4 * i;
+                    const float c = stage_q_row(v[i], sm.q[qb], r, NT + r, l, L.score_scale);
+                    if (l == 0)
+                        sm.c[qb][r] = c;
                 }
             }
             fence_proxy_async_smem();
@@ -294,163 +380,185 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------- softmax ----------------
-        // A wait that fails is voted on at the group's next barrier, so that its four warps leave
-        // together; a group that leaves, at the end of its work too, takes one turn at the barrier of
-        // both groups (kBarBoth), where the other one learns of it.
-        const uint32_t g = (warp >> 2) - 1, bar = 1 + g;
+        // A wait that fails is voted on at the next barrier of the group's half, so that its four warps
+        // leave together; a half that leaves, at the end of its work too, takes one turn at the barrier
+        // of all halves (kBarAll), where the others learn of it.
+        const uint32_t sub = (warp >> 2) - 1, g = sub >> 1, h4 = 4 * (sub & 1), bar = 1 + sub;
         const int qd = warp & 3, key = 32 * qd + lane; // this thread's key of a block, and dim of O^T
+        // its rows: 8 i + h4 + e, for e in 0..3 and i in 0..R8 - 1
         const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
-        const uint32_t s_addr = tmem + lanes + g * 2 * NT, o_addr = tmem + lanes + kColO + g * 3 * NT;
-        uint8_t *const pcol = sm.p[g] + (key & 15);
+        const uint32_t s_addr = tmem + lanes + g * 2 * NT + h4, o_addr = tmem + lanes + kColO + h4;
+        uint8_t *const pcol = sm.p[g] + h4 * 128 + (key & 15); // the key's byte in row h4 + e of a swizzle atom:
+        uint32_t off[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            off[e] = static_cast<uint32_t>(e * 128 + (((key >> 4) ^ (h4 + e)) << 4));
+        const float *const nm = sm.nm[g] + h4, *const alpha = sm.alpha[g] + h4;
         uint32_t c = 0; // blocks of the CTA before this tile
-        bool ok = true, both = false;
+        bool ok = true, left = false;
         for (uint32_t n = 0;; ++n) {
             ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
             if (bar_or(bar, 128, !ok))
                 break;
-            const Job j = sm.job[n % kJobs];
+            const Job &job = sm.job[n % kJobs];
+            const int nblk = job.nblk, blk0 = job.blk0, lo = job.lo, hi = job.hi, rows = job.rows, slot = job.slot;
             warp_arrive(&sm.job_empty[n % kJobs], lane);
-            if (j.nblk < 0)
+            if (nblk < 0)
                 break;
-            const uint32_t qb = n & 1u;
-            ok = warp_wait(&sm.q_full[qb], (n >> 1) & 1u, ab);
-            if (key < NT)
-                sm.cm[g][key] = make_float2(sm.c[qb][key], kNoMax);
+            const uint32_t qb = n % kQ;
+            ok = warp_wait(&sm.q_full[qb], (n / kQ) & 1u, ab);
+            if (key < NT && ((key ^ h4) & 4) == 0)
+                sm.nm[g][key] = key < rows ? -kNoMax : 0.f; // rows of padding score 0 and never move
             if (bar_or(bar, 128, !ok))
                 break;
-            const int R8 = (j.rows + 7) >> 3;                                     // groups of eight rows
-            const int pos_lo = sm.pos[qb][0], pos_hi = sm.pos[qb][j.rows - 1]; // first and last token
-            float l[NT];
+            const int R8 = (rows + 7) >> 3;                                 // groups of eight rows
+            const int pos_lo = sm.pos[qb][0], pos_hi = sm.pos[qb][rows - 1]; // first and last token
+            const float *const fac = sm.c[qb] + h4;
+            F2 l[NT / 8][2];
 #pragma unroll
-            for (int r = 0; r < NT; ++r)
-                l[r] = 0.f;
-            uint32_t used = 0, u = 0;
-            bool failed = false;
-            for (int k = static_cast<int>((c ^ g) & 1u); k < j.nblk; k += 2, ++used) {
+            for (int i = 0; i < NT / 8; ++i)
+                l[i][0] = l[i][1] = 0ull;
+            bool used = false, failed = false;
+            uint32_t u = 0;
+            for (int k = static_cast<int>((c ^ g) & 1u); k < nblk; k += 2, used = true) {
                 const uint32_t cc = c + k, s = cc % kSt;
                 u = cc >> 1;
-                const int b0 = (j.blk0 + k) * kBlock, kp = b0 + key; // this thread's position
-                // some row does not see the whole block
-                const bool edge = b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window);
+                const int b0 = (blk0 + k) * kBlock, kp = b0 + key; // this thread's position
                 ok = warp_wait(&sm.s_done[g], u & 1u, ab);
                 tc_fence_after();
-                float y[NT]; // base-2 exponents
-                float top = -INFINITY;
+                F2 y[NT / 8][2]; // base-2 exponents
+                bool over = false;
 #pragma unroll
-                for (int r8 = 0; r8 < NT / 8; ++r8)
-                    if (r8 < R8) {
-                        uint32_t a[8], b[8];
-                        tmem_ld8(s_addr + 8 * r8, a);
-                        tmem_ld8(s_addr + NT + 8 * r8, b);
-                        tmem_wait8(a);
-                        tmem_wait8(b);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int r = 8 * r8 + e;
-                            const float2 cm = sm.cm[g][r];
-                            y[r] = (__uint_as_float(a[e]) + __uint_as_float(b[e])) * cm.x;
-                            if (edge) {
-                                const int pr = sm.pos[qb][r];
-                                if (kp > pr || (L.window > 0 && kp <= pr - L.window))
-                                    y[r] = -INFINITY;
-                            }
-                            if (r < j.rows)
-                                top = fmaxf(top, y[r] - cm.y);
-                        }
+                for (int i = 0; i < NT / 8; ++i)
+                    if (i < R8) {
+                        uint32_t a[4], b[4];
+                        tmem_ld4(s_addr + 8 * i, a);
+                        tmem_ld4(s_addr + NT + 8 * i, b);
+                        tmem_wait(a);
+                        tmem_wait(b);
+                        const float4 f = *reinterpret_cast<const float4 *>(fac + 8 * i);
+                        y[i][0] = mul2(add2(pack2(__uint_as_float(a[0]), __uint_as_float(a[1])),
+                                            pack2(__uint_as_float(b[0]), __uint_as_float(b[1]))), pack2(f.x, f.y));
+                        y[i][1] = mul2(add2(pack2(__uint_as_float(a[2]), __uint_as_float(a[3])),
+                                            pack2(__uint_as_float(b[2]), __uint_as_float(b[3]))), pack2(f.z, f.w));
                     }
                 tc_fence_before();
                 warp_arrive(&sm.s_free[g], lane);
-                if (bar_or(bar, 128, !ok || top > kRaise)) {
+                // some row does not see the whole block
+                if (b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window)) {
+#pragma unroll
+                    for (int i = 0; i < NT / 8; ++i)
+                        if (i < R8) {
+                            const int4 pr = *reinterpret_cast<const int4 *>(sm.pos[qb] + 8 * i + h4);
+                            const int w = L.window > 0 ? L.window : 0x7FFFFFFF; // key kp is seen from kp to kp + w - 1
+                            float x0, x1;
+                            unpack2(y[i][0], x0, x1);
+                            x0 = pr.x >= kp && pr.x - kp < w ? x0 : -INFINITY;
+                            x1 = pr.y >= kp && pr.y - kp < w ? x1 : -INFINITY;
+                            y[i][0] = pack2(x0, x1);
+                            unpack2(y[i][1], x0, x1);
+                            x0 = pr.z >= kp && pr.z - kp < w ? x0 : -INFINITY;
+                            x1 = pr.w >= kp && pr.w - kp < w ? x1 : -INFINITY;
+                            y[i][1] = pack2(x0, x1);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < NT / 8; ++i)
+                    if (i < R8) {
+                        const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(nm + 8 * i);
+                        float x0, x1, x2, x3;
+                        unpack2(add2(y[i][0], m.x), x0, x1);
+                        unpack2(add2(y[i][1], m.y), x2, x3);
+                        over = over || fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) > kRaise;
+                    }
+                if (bar_or(bar, 128, !ok || over)) {
                     // The block's maximum of every row; where it exceeds the reference by more than
                     // kRaise, the reference moves and what the row has so far is scaled.
 #pragma unroll
-                    for (int r = 0; r < NT; ++r)
-                        if (r < j.rows) {
-                            float m = y[r];
-#pragma unroll
-                            for (int d = 16; d > 0; d >>= 1)
-                                m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+                    for (int i = 0; i < NT / 8; ++i)
+                        if (i < R8) {
+                            float4 m;
+                            unpack2(y[i][0], m.x, m.y);
+                            unpack2(y[i][1], m.z, m.w);
+                            m = make_float4(warp_max(m.x), warp_max(m.y), warp_max(m.z), warp_max(m.w));
                             if (lane == 0)
-                                sm.red[g][qd][r] = m;
+                                *reinterpret_cast<float4 *>(&sm.red[g][qd][8 * i + h4]) = m;
                         }
-                    if (ok && used > 0) // the products so far
+                    if (ok && used) // the products so far
                         ok = warp_wait(&sm.pv_done[g], (u - 1) & 1u, ab);
                     if (bar_or(bar, 128, !ok)) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
-#pragma unroll
-                    for (int r8 = 0; r8 < NT / 8; ++r8)
-                        if (r8 < R8) {
-                            float alpha[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int r = 8 * r8 + e;
-                                const float m = sm.cm[g][r].y;
-                                const float top_r = fmaxf(fmaxf(sm.red[g][0][r], sm.red[g][1][r]),
-                                                          fmaxf(sm.red[g][2][r], sm.red[g][3][r]));
-                                alpha[e] = r < j.rows && top_r - m > kRaise ? attn::ex2(m - (top_r - kBelow)) : 1.f;
-                                l[r] *= alpha[e];
-                            }
-                            if (used > 0) {
-#pragma unroll
-                                for (int part = 0; part < 3; ++part) {
-                                    uint32_t o[8];
-                                    tmem_ld8(o_addr + part * NT + 8 * r8, o);
-                                    tmem_wait8(o);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e]);
-                                    tmem_st8(o_addr + part * NT + 8 * r8, o);
-                                }
-                            }
-                        }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    bar_sync(bar, 128); // every thread has read the old references
-                    if (key < j.rows) {
-                        const float top_r = fmaxf(fmaxf(sm.red[g][0][key], sm.red[g][1][key]),
-                                                  fmaxf(sm.red[g][2][key], sm.red[g][3][key]));
-                        if (top_r - sm.cm[g][key].y > kRaise)
-                            sm.cm[g][key].y = top_r - kBelow;
+                    if (key < NT && ((key ^ h4) & 4) == 0) { // a thread a row
+                        const float top = fmaxf(fmaxf(sm.red[g][0][key], sm.red[g][1][key]), fmaxf(sm.red[g][2][key], sm.red[g][3][key]));
+                        const float m = sm.nm[g][key];
+                        const bool move = key < rows && top + m > kRaise;
+                        sm.alpha[g][key] = move ? attn::ex2(kBelow - top - m) : 1.f;
+                        if (move)
+                            sm.nm[g][key] = kBelow - top;
                     }
                     bar_sync(bar, 128);
+#pragma unroll
+                    for (int i = 0; i < NT / 8; ++i)
+                        if (i < R8) {
+                            const ulonglong2 al = *reinterpret_cast<const ulonglong2 *>(alpha + 8 * i);
+                            l[i][0] = mul2(l[i][0], al.x);
+                            l[i][1] = mul2(l[i][1], al.y);
+                        }
+                    if (used) {
+#pragma unroll 1
+                        for (int i = 0; i < R8; ++i) {
+                            const float4 al = *reinterpret_cast<const float4 *>(alpha + 8 * i);
+#pragma unroll 1
+                            for (int part = 0; part < 3; ++part) {
+                                const uint32_t at = o_addr + (g * 3 + part) * NT + 8 * i;
+                                uint32_t o[4];
+                                tmem_ld4(at, o);
+                                tmem_wait(o);
+                                o[0] = __float_as_uint(__uint_as_float(o[0]) * al.x);
+                                o[1] = __float_as_uint(__uint_as_float(o[1]) * al.y);
+                                o[2] = __float_as_uint(__uint_as_float(o[2]) * al.z);
+                                o[3] = __float_as_uint(__uint_as_float(o[3]) * al.w);
+                                tmem_st4(at, o);
+                            }
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
                 }
-                // the group's last products have read its weights (and, at a tile's start, the
-                // previous tile's accumulator has been read)
+                // the group's last products have read its weights
                 if (cc >= 2)
                     ok = warp_wait(&sm.pv_done[g], (u - 1) & 1u, ab);
-                uint32_t off[8]; // this key's byte in rows 0..7 of a swizzle atom
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    off[e] = static_cast<uint32_t>(e * 128 + (((key >> 4) ^ e) << 4));
+                for (int i = 0; i < NT / 8; ++i)
+                    if (i < R8) {
+                        const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(nm + 8 * i);
 #pragma unroll
-                for (int r8 = 0; r8 < NT / 8; ++r8)
-                    if (r8 < R8) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const int r = 8 * r8 + e;
-                            const float p0 = attn::ex2(y[r] - sm.cm[g][r].y), p1 = attn::ex2(y[r + 1] - sm.cm[g][r + 1].y);
-                            l[r] += p0;
-                            l[r + 1] += p1;
+                        for (int e = 0; e < 2; ++e) {
+                            float p0, p1;
+                            unpack2(add2(y[i][e], e == 0 ? m.x : m.y), p0, p1);
+                            p0 = attn::ex2(p0);
+                            p1 = attn::ex2(p1);
+                            l[i][e] = add2(l[i][e], pack2(p0, p1));
                             uint32_t w[3];
-                            split3(p0, p1, w[0], w[1], w[2]);
+                            split3(p0, p1, w);
 #pragma unroll
                             for (int part = 0; part < 3; ++part) {
-                                uint8_t *const at = pcol + (part * NT + 8 * r8) * 128;
-                                at[off[e]] = static_cast<uint8_t>(w[part]);
-                                at[off[e + 1]] = static_cast<uint8_t>(w[part] >> 8);
+                                uint8_t *const at = pcol + (part * NT + 8 * i) * 128;
+                                at[off[2 * e]] = static_cast<uint8_t>(w[part]);
+                                at[off[2 * e + 1]] = static_cast<uint8_t>(w[part] >> 8);
                             }
                         }
                     }
                 // Values of keys that no row of the tile sees may be any bytes, NaN codes among them,
                 // and zero times NaN is not zero: they become zeros before the products read them.
-                if (b0 < j.lo || b0 + kBlock > j.hi) {
+                if (h4 == 0 && (b0 < lo || b0 + kBlock > hi)) {
                     ok = warp_wait(&sm.v_full[s], (cc / kSt) & 1u, ab) && ok;
-                    if (kp < j.lo || kp >= j.hi) {
+                    if (kp < lo || kp >= hi) {
                         uint4 *row = reinterpret_cast<uint4 *>(sm.v[s] + key * 128);
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < 8; ++i)
                             row[i] = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -460,77 +568,89 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (failed)
                 break;
-            // ---- the end of the tile: sums over the keys, group 1's part to group 0, the result ----
-            if (ok && used > 0)
+            // ---- the end of the tile ----
+            // Sums over the 32 keys of a warp: a lane gives half of its rows away twice, then the
+            // lanes that hold the same row add up.
+#pragma unroll
+            for (int i = 0; i < NT / 8; ++i)
+                if (i < R8) {
+                    float x0, x1, x2, x3;
+                    unpack2(l[i][0], x0, x1);
+                    unpack2(l[i][1], x2, x3);
+                    const bool up = lane & 16, odd = lane & 8;
+                    const float k0 = up ? x2 : x0, k1 = up ? x3 : x1;
+                    const float y0 = k0 + __shfl_xor_sync(kFull, up ? x0 : x2, 16), y1 = k1 + __shfl_xor_sync(kFull, up ? x1 : x3, 16);
+                    float z = (odd ? y1 : y0) + __shfl_xor_sync(kFull, odd ? y0 : y1, 8);
+                    z += __shfl_xor_sync(kFull, z, 4);
+                    z += __shfl_xor_sync(kFull, z, 2);
+                    z += __shfl_xor_sync(kFull, z, 1);
+                    if ((lane & 7) == 0)
+                        sm.red[g][qd][8 * i + h4 + (lane >> 3)] = z;
+                }
+            if (ok && used)
                 ok = warp_wait(&sm.pv_done[g], u & 1u, ab);
-            tc_fence_after();
-            float o[NT];
-#pragma unroll
-            for (int r8 = 0; r8 < NT / 8; ++r8) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    o[8 * r8 + e] = 0.f;
-                if (r8 < R8 && used > 0) {
-                    uint32_t a[8], b[8], d[8];
-                    tmem_ld8(o_addr + 8 * r8, a);
-                    tmem_ld8(o_addr + NT + 8 * r8, b);
-                    tmem_ld8(o_addr + 2 * NT + 8 * r8, d);
-                    tmem_wait8(a);
-                    tmem_wait8(b);
-                    tmem_wait8(d);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[8 * r8 + e] = fmaf(fmaf(__uint_as_float(d[e]), 0.0625f, __uint_as_float(b[e])), 0.0625f,
-                                             __uint_as_float(a[e]));
-                }
-            }
             tc_fence_before();
-#pragma unroll
-            for (int r = 0; r < NT; ++r)
-                if (r < j.rows) {
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1)
-                        l[r] += __shfl_xor_sync(kFull, l[r], d);
-                    if (lane == 0)
-                        sm.red[g][qd][r] = l[r];
-                    if (g == 1)
-                        sm.stage[r][key] = o[r];
-                }
-            if (bar_or(kBarBoth, 256, !ok)) {
-                both = true;
+            if (bar_or(kBarAll, kSoftmax, !ok)) {
+                left = true;
                 break;
             }
-            float *part = j.slot >= 0 ? partial<NT>(L, cta, j.slot) : nullptr;
-            if (g == 0) {
+            tc_fence_after();
+            // Each half of a group joins the accumulators of both for two of its four rows.
+            float *const part = slot >= 0 ? partial<NT>(L, cta, slot) : nullptr;
+            const bool both = nblk > 1;
+#pragma unroll 1
+            for (int i = 0; i < R8; ++i) {
+                const int r = 8 * i + h4 + 2 * static_cast<int>(g); // rows r and r + 1
+                if (r >= rows)
+                    break;
+                float o[2][2];
 #pragma unroll
-                for (int r = 0; r < NT; ++r)
-                    if (r < j.rows) {
-                        const float m0 = sm.cm[0][r].y, m1 = sm.cm[1][r].y, m = fmaxf(m0, m1);
+                for (int gg = 0; gg < 2; ++gg) {
+                    o[gg][0] = o[gg][1] = 0.f;
+                    if (both || static_cast<uint32_t>(gg) == (c & 1u)) { // the group has had a block
+                        const uint32_t at = o_addr + gg * 3 * NT + 8 * i + 2 * g;
+                        uint32_t x[2], y[2], z[2];
+                        tmem_ld2(at, x);
+                        tmem_ld2(at + NT, y);
+                        tmem_ld2(at + 2 * NT, z);
+                        tmem_wait(x);
+                        tmem_wait(y);
+                        tmem_wait(z);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            o[gg][e] = fmaf(fmaf(__uint_as_float(z[e]), 0.0625f, __uint_as_float(y[e])), 0.0625f, __uint_as_float(x[e]));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (r + e < rows) {
+                        const int rr = r + e;
+                        const float m0 = -sm.nm[0][rr], m1 = -sm.nm[1][rr], m = fmaxf(m0, m1);
                         const float a0 = attn::ex2(m0 - m), a1 = attn::ex2(m1 - m);
-                        const float sum = a0 * ((sm.red[0][0][r] + sm.red[0][1][r]) + (sm.red[0][2][r] + sm.red[0][3][r])) +
-                                          a1 * ((sm.red[1][0][r] + sm.red[1][1][r]) + (sm.red[1][2][r] + sm.red[1][3][r]));
-                        const float v = a0 * o[r] + a1 * sm.stage[r][key];
+                        const float sum = a0 * ((sm.red[0][0][rr] + sm.red[0][1][rr]) + (sm.red[0][2][rr] + sm.red[0][3][rr])) +
+                                          a1 * ((sm.red[1][0][rr] + sm.red[1][1][rr]) + (sm.red[1][2][rr] + sm.red[1][3][rr]));
+                        const float v = a0 * o[0][e] + a1 * o[1][e];
                         if (part != nullptr) {
-                            part[r * kHeadDim + key] = v;
-                            if (key == r) {
-                                part[NT * kHeadDim + r] = m;
-                                part[NT * (kHeadDim + 1) + r] = sum;
+                            part[rr * kHeadDim + key] = v;
+                            if (key == 0) {
+                                part[NT * kHeadDim + rr] = m;
+                                part[NT * (kHeadDim + 1) + rr] = sum;
                             }
                         } else {
-                            const int flat = j.row + r, tok = flat / L.G;
-                            const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
+                            const int64_t at = sm.at[qb][rr];
                             L.O[at * kHeadDim + key] = __bfloat16_as_ushort(__float2bfloat16_rn(v * (L.v_scale / sum)));
-                            if (L.lse != nullptr && key == r)
+                            if (L.lse != nullptr && key == 0)
                                 L.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
                         }
                     }
             }
-            warp_arrive(&sm.q_empty[qb], lane); // positions and factors read
-            bar_sync(kBarBoth, 256); // group 0 has read the staged part and the references
-            c += j.nblk;
+            tc_fence_before();
+            warp_arrive(&sm.q_empty[qb], lane); // positions, places and factors read
+            bar_sync(kBarAll, kSoftmax);        // references, sums and accumulators read
+            c += nblk;
         }
-        if (!both)
-            (void)bar_or(kBarBoth, 256, true);
+        if (!left)
+            (void)bar_or(kBarAll, kSoftmax, true);
     }
 
     tc_fence_before();
