@@ -109,7 +109,12 @@ struct Plan {
     int64_t scan[33];
 };
 
-__device__ __forceinline__ int64_t stretch(int64_t total, int ctas, int j) { return total * j / ctas; }
+// First block of stretch j: equal stretches, the first ones one longer.
+__device__ __forceinline__ int64_t stretch(int64_t total, int ctas, int j)
+{
+    const int64_t q = total / ctas;
+    return q * j + min(static_cast<int64_t>(j), total - q * ctas);
+}
 
 // Block-wide inclusive scan of v; returns it and the sum in `sum`.  scratch: 33 words.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64_t &sum)
@@ -436,11 +441,14 @@ cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap 
 cudaError_t decode_launch(const ChunkLaunch &L, int rows, int ctas, cudaStream_t st);
 size_t decode_workspace(int rows);
 
-// Joins the partial results of the tiles that were cut: the block of stretch j does the tile that
-// the stretch starts inside of, unless an earlier stretch starts inside of it too.  One warp per row.
+// Joins the partial results of the tiles that were cut: block j does the tile that stretch j starts
+// inside of, unless an earlier stretch starts inside of it too.  One warp per row.  Its blocks are
+// brought up while the attention kernel still runs (programmatic launch; 128 threads of 32
+// registers fit beside it) and wait for its end.
 template <int NT>
-__global__ void __launch_bounds__(128) k_chunk_merge(const ChunkLaunch L)
+__global__ void __launch_bounds__(128, 16) k_chunk_merge(const ChunkLaunch L)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int j = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
     const Cut c = reinterpret_cast<const Cut *>(L.workspace)[j];
     if (!c.inside || r >= c.rows || stretch(c.total, c.ctas, j - 1) > c.ts)
@@ -489,11 +497,22 @@ __global__ void __launch_bounds__(128) k_chunk_merge(const ChunkLaunch L)
         L.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+// Lets k_chunk_merge come up; every thread of the attention kernels calls it.
+__device__ __forceinline__ void allow_merge() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <int NT>
 cudaError_t merge_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
 {
-    k_chunk_merge<NT><<<dim3(ctas, (NT + 3) / 4), 128, 0, st>>>(L);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas, (NT + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_chunk_merge<NT>, L);
 }
 
 } // namespace chunk

@@ -5,15 +5,17 @@
 //   S^T = K [q1 q2]        (M = keys, N = 2 NT, K = 128 dims; E4M3)
 //   O^T += V^T [P1 P2 P3]  (M = dims, N = 3 NT, K = 128 keys; E4M3, V read as stored, MN-major)
 // straight from the bytes that TMA landed.  Queries enter as two exact E4M3 parts (pw_chunk.cuh),
-// weights as three, each the remainder of the one before times 2^4 and rounded to 4 significant
-// bits: together 12 bits (a relative 2^-12, half the error of one f16) of a weight of at least 2^-6
-// and an absolute 2^-18 below, at no more passes over V, since the parts lie side by side along N.
+// weights, rounded to f16, as three exact ones: four significant bits, the next four of what is left,
+// and the rest, at no more passes over V, since the parts lie side by side along N.  A weight of at
+// most 1 whose f16 bits are shifted right by 7 is the E4M3 code of 2^8 times the weight, cut off, with
+// the subnormal numbers of both formats in the same places, so a part is a shift and a subtraction
+// (conversions to and from E4M3 run at the rate of the exponential and took twice its time).
 //
-// The running maximum of a row is a reference that only has to keep its weights in range: it moves
-// when a score exceeds it by more than 2^8 (256 stays inside E4M3's 448), to 2^4 below that score,
-// so that the largest weight lies in [2^4, 2^8] and the absolute error of the small ones is 2^-22
-// of it.  That costs one vote per block instead of a reduction over the keys, which lie along the
-// threads here.
+// The running maximum of a row is a reference that only has to keep its weights in range: it lies
+// above the scores and moves when one exceeds it, to 4 (base 2) above that score, so that a row's
+// largest weight lies in [2^-4, 1] and the smallest step of f16 (2^-24, weights below 2^-14) is at most
+// 2^-20 of it.  That costs one vote per block instead of a reduction over the keys, which lie along
+// the threads here.
 //
 // Two groups of eight softmax warps take blocks in turn (block c goes to group c % 2), each with its
 // own S, P, accumulator, reference and sums; they meet at the end of a tile.  The two warps of a
@@ -47,8 +49,7 @@ constexpr int kJobs = 4;
 constexpr int kQ = 3;
 constexpr int kMinBlocks = 1;
 constexpr uint32_t kBarAll = 5; // named barrier of all softmax warps (the groups' halves: 1 to 4)
-constexpr float kRaise = 8.f; // a row's reference moves when a score exceeds it by more (base 2),
-constexpr float kBelow = 4.f; // to this much below that score
+constexpr float kAbove = 4.f;  // a row's reference moves to this much above its largest score (base 2)
 
 template <int NT> constexpr int kStagesFor = NT == 16 ? 6 : 5;
 
@@ -57,7 +58,9 @@ struct __align__(1024) DecSmem {
     static constexpr int kStages = kStagesFor<NT>;
     uint8_t k[kStages][kBlock * 128]; // 128 keys x 128 dims
     uint8_t v[kStages][kBlock * 128];
-    uint8_t p[2][3 * NT * 128];       // [group][part, row][key]
+    // [group]: the weights as a matrix of 3 NT columns (part, row) by 128 keys, columns contiguous:
+    // cores of 8 keys by 16 columns (128 bytes), the cores of the same 8 keys side by side
+    uint8_t p[2][3 * NT * 128];
     uint8_t q[kQ][2 * NT * 128];      // [tile % kQ][part, row][dim]
     float c[kQ][NT];                  // [tile % kQ]: factor of a row's scores
     int pos[kQ][NT];                  // [tile % kQ]: position of the row's token
@@ -102,24 +105,17 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b)
     return d;
 }
 
-// One key's weights of two rows, rounded to f16 and split exactly into three E4M3 parts each (byte
-// 0: the first row's), the second and third times 2^4 and 2^8.
+// One key's weights of two rows, 0..1, rounded to f16 and cut exactly into three E4M3 parts each, the
+// second and third times 2^4 and 2^8: bits 7..14 and 23..30 of w hold the codes of the two rows.
 __device__ __forceinline__ void split3(float p0, float p1, uint32_t (&w)[3])
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(p1), "f"(p0));
-    __half2 x = *reinterpret_cast<__half2 *>(&h);
-    const __half2 k16 = __float2half2_rn(16.f);
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(p1), "f"(p0));
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        uint16_t e;
-        uint32_t y;
-        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<uint32_t *>(&x)));
-        w[i] = e;
-        if (i < 2) {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(e));
-            x = __hmul2(__hsub2(x, *reinterpret_cast<__half2 *>(&y)), k16);
-        }
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t cut = w[i] & 0xFF80FF80u;
+        const __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&w[i]), *reinterpret_cast<const __half2 *>(&cut));
+        const __half2 r = __hmul2(rest, __float2half2_rn(16.f));
+        w[i + 1] = *reinterpret_cast<const uint32_t *>(&r);
     }
 }
 
@@ -168,11 +164,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kTmemCols = NT == 16 ? 256 : 512;
     constexpr uint32_t kColO = 4 * NT; // S of the two groups, then their accumulators
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 2 * NT);
-    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, 3 * NT) | (1u << 15); // A (V^T) MN-major
+    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, 3 * NT) | (1u << 15) | (1u << 16); // A (V^T) and B (P) MN-major
+    constexpr int kKeys8 = 3 * NT * 8; // bytes of P of 8 keys
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
 
+    allow_merge();
     if (tid == 0) {
         for (int i = 0; i < kJobs; ++i) {
             mbar_init(&sm.job_full[i], 1);
@@ -280,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // also across the end of a tile: its S is read by then, so it computes while that group forms
         // its weights.
         const uint64_t dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024), dv = sdesc_sw128(smem_u32(sm.v[0]), 16, 1024);
-        const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dp = sdesc_sw128(smem_u32(sm.p[0]), 16, 1024);
+        const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dp = sdesc_plain(smem_u32(sm.p[0]), kKeys8, 128);
         uint32_t c = 0;
         bool ok = true;
         // products of block cc, the first of its group in the tile or not
@@ -293,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_f8_ss(tmem + kColO + g * 3 * NT, dv + ((s * kBlock * 128 + kk * 32 * 128) >> 4),
-                              dp + ((g * 3 * NT * 128 + kk * 32) >> 4), kIdescO, kk > 0 || !first);
+                              dp + ((g * 3 * NT * 128 + kk * 4 * kKeys8) >> 4), kIdescO, kk > 0 || !first);
                 mma_commit(&sm.pv_done[g]);
                 mma_commit(&sm.st_empty[s]);
             }
@@ -388,11 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // its rows: 8 i + h4 + e, for e in 0..3 and i in 0..R8 - 1
         const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
         const uint32_t s_addr = tmem + lanes + g * 2 * NT + h4, o_addr = tmem + lanes + kColO + h4;
-        uint8_t *const pcol = sm.p[g] + h4 * 128 + (key & 15); // the key's byte in row h4 + e of a swizzle atom:
-        uint32_t off[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            off[e] = static_cast<uint32_t>(e * 128 + (((key >> 4) ^ (h4 + e)) << 4));
+        uint8_t *const pcol = sm.p[g] + (key >> 3) * kKeys8 + (key & 7) * 16;
         const float *const nm = sm.nm[g] + h4, *const alpha = sm.alpha[g] + h4;
         uint32_t c = 0; // blocks of the CTA before this tile
         bool ok = true, left = false;
@@ -429,18 +423,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 F2 y[NT / 8][2]; // base-2 exponents
                 bool over = false;
 #pragma unroll
-                for (int i = 0; i < NT / 8; ++i)
-                    if (i < R8) {
-                        uint32_t a[4], b[4];
-                        tmem_ld4(s_addr + 8 * i, a);
-                        tmem_ld4(s_addr + NT + 8 * i, b);
-                        tmem_wait(a);
-                        tmem_wait(b);
-                        const float4 f = *reinterpret_cast<const float4 *>(fac + 8 * i);
-                        y[i][0] = mul2(add2(pack2(__uint_as_float(a[0]), __uint_as_float(a[1])),
-                                            pack2(__uint_as_float(b[0]), __uint_as_float(b[1]))), pack2(f.x, f.y));
-                        y[i][1] = mul2(add2(pack2(__uint_as_float(a[2]), __uint_as_float(a[3])),
-                                            pack2(__uint_as_float(b[2]), __uint_as_float(b[3]))), pack2(f.z, f.w));
+                for (int i0 = 0; i0 < NT / 8; i0 += 2)
+                    if (i0 < R8) {
+                        uint32_t a[2][4], b[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            tmem_ld4(s_addr + 8 * (i0 + i), a[i]);
+                            tmem_ld4(s_addr + NT + 8 * (i0 + i), b[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            tmem_wait(a[i]);
+                            tmem_wait(b[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 f = *reinterpret_cast<const float4 *>(fac + 8 * (i0 + i));
+                            y[i0 + i][0] = mul2(add2(pack2(__uint_as_float(a[i][0]), __uint_as_float(a[i][1])),
+                                                     pack2(__uint_as_float(b[i][0]), __uint_as_float(b[i][1]))), pack2(f.x, f.y));
+                            y[i0 + i][1] = mul2(add2(pack2(__uint_as_float(a[i][2]), __uint_as_float(a[i][3])),
+                                                     pack2(__uint_as_float(b[i][2]), __uint_as_float(b[i][3]))), pack2(f.z, f.w));
+                        }
                     }
                 tc_fence_before();
                 warp_arrive(&sm.s_free[g], lane);
@@ -469,11 +472,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float x0, x1, x2, x3;
                         unpack2(add2(y[i][0], m.x), x0, x1);
                         unpack2(add2(y[i][1], m.y), x2, x3);
-                        over = over || fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) > kRaise;
+                        over = over || fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) > 0.f;
                     }
                 if (bar_or(bar, 128, !ok || over)) {
-                    // The block's maximum of every row; where it exceeds the reference by more than
-                    // kRaise, the reference moves and what the row has so far is scaled.
+                    // The block's maximum of every row; where it exceeds the reference, the reference
+                    // moves and what the row has so far is scaled.
 #pragma unroll
                     for (int i = 0; i < NT / 8; ++i)
                         if (i < R8) {
@@ -494,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (key < NT && ((key ^ h4) & 4) == 0) { // a thread a row
                         const float top = fmaxf(fmaxf(sm.red[g][0][key], sm.red[g][1][key]), fmaxf(sm.red[g][2][key], sm.red[g][3][key]));
                         const float m = sm.nm[g][key];
-                        const bool move = key < rows && top + m > kRaise;
-                        sm.alpha[g][key] = move ? attn::ex2(kBelow - top - m) : 1.f;
+                        const bool move = key < rows && top + m > 0.f;
+                        sm.alpha[g][key] = move ? attn::ex2(-(top + kAbove) - m) : 1.f;
                         if (move)
-                            sm.nm[g][key] = kBelow - top;
+                            sm.nm[g][key] = -(top + kAbove);
                     }
                     bar_sync(bar, 128);
 #pragma unroll
@@ -535,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < NT / 8; ++i)
                     if (i < R8) {
                         const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(nm + 8 * i);
+                        uint32_t w[2][3];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float p0, p1;
@@ -542,14 +546,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p0 = attn::ex2(p0);
                             p1 = attn::ex2(p1);
                             l[i][e] = add2(l[i][e], pack2(p0, p1));
-                            uint32_t w[3];
-                            split3(p0, p1, w);
+                            split3(p0, p1, w[e]);
+                        }
 #pragma unroll
-                            for (int part = 0; part < 3; ++part) {
-                                uint8_t *const at = pcol + (part * NT + 8 * i) * 128;
-                                at[off[2 * e]] = static_cast<uint8_t>(w[part]);
-                                at[off[2 * e + 1]] = static_cast<uint8_t>(w[part] >> 8);
-                            }
+                        for (int part = 0; part < 3; ++part) { // the codes of the four rows
+                            const int n = part * NT + 8 * i;   // first column of the eight
+                            *reinterpret_cast<uint32_t *>(pcol + n / 16 * 128 + n % 16 + h4) =
+                                attn::prmt(w[0][part] >> 7, w[1][part] >> 7, 0x6420u);
                         }
                     }
                 // Values of keys that no row of the tile sees may be any bytes, NaN codes among them,
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait(z);
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            o[gg][e] = fmaf(fmaf(__uint_as_float(z[e]), 0.0625f, __uint_as_float(y[e])), 0.0625f, __uint_as_float(x[e]));
+                            o[gg][e] = fmaf(fmaf(__uint_as_float(z[e]), 0x1p-4f, __uint_as_float(y[e])), 0x1p-4f, __uint_as_float(x[e])) * 0x1p-8f;
                     }
                 }
 #pragma unroll

@@ -294,6 +294,19 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     return d;
 }
 
+// Shared-memory matrix descriptor without swizzle, sm_100 version field, for an MN-major tile of
+// cores (8 along K by 16 bytes along M/N, 128 bytes each): `kstride` bytes between cores along K,
+// `mnstride` along M/N.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t kstride, uint32_t mnstride)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((kstride >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((mnstride >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46; // descriptor version for sm_100
+    return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16: f16 x f16 -> f32, dense.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major)
 {
