@@ -1,112 +1,13 @@
-// pw_chunk.cu -- pw_chunk_attn: causal attention of new tokens over the paged E4M3 cache.
-//
-// One warp per (row, query head): 32 keys at a time, lane d4 holds four dimensions of q, k and v;
-// the scores of the 32 keys go to one lane each, the softmax is online in fp32, base 2.
+// pw_chunk.cu -- pw_chunk_attn: causal attention of new tokens over the paged E4M3 cache; which
+// kernel a call takes, and what they need from the host.
+#include <algorithm>
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "pw_chunk.cuh"
 
 namespace pw {
-namespace {
-
-using namespace tokens;
-constexpr uint32_t kFull = 0xFFFFFFFFu;
-
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t x, float (&f)[4])
-{
-    uint32_t a, b;
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}\n"
-        : "=r"(a), "=r"(b) : "r"(x));
-    const __half2 p = *reinterpret_cast<const __half2 *>(&a), q = *reinterpret_cast<const __half2 *>(&b);
-    f[0] = __low2float(p);
-    f[1] = __high2float(p);
-    f[2] = __low2float(q);
-    f[3] = __high2float(q);
-}
-
-__global__ void __launch_bounds__(256) k_chunk_rows(const ChunkLaunch L)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t t = w / L.Hq;
-    const int hq = static_cast<int>(w - t * L.Hq), h = hq / L.G;
-    if (t >= L.tb.T)
-        return;
-    const int b = find_sequence(L.tb, t, lane);
-    if (b >= L.tb.B)
-        return;
-    const int64_t i = t - L.tb.cu[b];
-    if (i < 0)
-        return;
-    int64_t pos = i + (L.tb.ctx != nullptr ? L.tb.ctx[b] : 0);
-    if (pos < 0 || pos >= static_cast<int64_t>(L.pm.max_pages) * 64) {
-        set_status(L.status, PW_ERR_INVALID_ARG);
-        pos = min(max(pos, static_cast<int64_t>(0)), static_cast<int64_t>(L.pm.max_pages) * 64 - 1);
-    }
-    const int64_t first = L.window > 0 ? max(pos - L.window + 1, static_cast<int64_t>(0)) : 0;
-    const uint2 qr = *reinterpret_cast<const uint2 *>(L.Q + t * L.q_st + hq * L.q_sh + 4 * lane);
-    const float c = L.score_scale;
-    const float q[4] = {bf16_lo(qr.x) * c, bf16_hi(qr.x) * c, bf16_lo(qr.y) * c, bf16_hi(qr.y) * c};
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t k0 = first & ~31ll; k0 <= pos; k0 += 32) {
-        int phys = L.pm.table[static_cast<int64_t>(b) * L.pm.max_pages + (k0 >> 6)];
-        if (phys < 0 || phys >= L.pm.n_phys) {
-            set_status(L.status, PW_ERR_INVALID_ARG);
-            phys = 0;
-        }
-        const size_t row = (static_cast<size_t>(phys) * L.Hkv + h) * 64 + (k0 & 63);
-        float s = -INFINITY;
-#pragma unroll 4
-        for (int j = 0; j < 32; ++j) {
-            float k[4];
-            e4m3x4_to_f32(reinterpret_cast<const uint32_t *>(L.K + (row + j) * 128)[lane], k);
-            float d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1)
-                d += __shfl_xor_sync(kFull, d, x);
-            if (lane == j && k0 + j >= first && k0 + j <= pos)
-                s = d;
-        }
-        float mx = s;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-        mx = fmaxf(mx, m);
-        const float a = exp2f(m - mx), p = exp2f(s - mx);
-        m = mx;
-        l = l * a + p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o[e] *= a;
-#pragma unroll 4
-        for (int j = 0; j < 32; ++j) {
-            const float pj = __shfl_sync(kFull, p, j);
-            if (k0 + j < first || k0 + j > pos)
-                continue;
-            float v[4];
-            e4m3x4_to_f32(reinterpret_cast<const uint32_t *>(L.V + (row + j) * 128)[lane], v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = fmaf(pj, v[e], o[e]);
-        }
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        l += __shfl_xor_sync(kFull, l, x);
-    const float inv = L.v_scale / l;
-    const __nv_bfloat162 r0 = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), r1 = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2 *>(L.O + (t * L.Hq + hq) * 128 + 4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&r0), *reinterpret_cast<const uint32_t *>(&r1));
-    if (L.lse != nullptr && lane == 0)
-        L.lse[t * L.Hq + hq] = (m + log2f(l)) * 0.6931471805599453f;
-}
-
-} // namespace
-
 namespace chunk {
 
 namespace {
@@ -149,9 +50,19 @@ cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap 
 
 } // namespace chunk
 
+namespace {
+
+// Rows of the longest chunk that share a kv head, up to which the kernel for few rows is taken.
+constexpr int64_t kFewRows = 64;
+
+int64_t rows_of(int Hq, int Hkv, int max_q_len) { return static_cast<int64_t>(max_q_len) * (Hq / Hkv); }
+
+} // namespace
+
 size_t chunk_workspace(int, int64_t, int Hq, int Hkv, int max_q_len)
 {
-    return chunk::decode_workspace(static_cast<int>(min(static_cast<int64_t>(max_q_len) * (Hq / Hkv), static_cast<int64_t>(1) << 20)));
+    const int64_t rows = rows_of(Hq, Hkv, max_q_len);
+    return rows <= kFewRows ? chunk::decode_workspace(static_cast<int>(rows)) : chunk::tiles_workspace();
 }
 
 cudaError_t chunk_launch(const ChunkLaunch &L, cudaStream_t st)
@@ -162,11 +73,9 @@ cudaError_t chunk_launch(const ChunkLaunch &L, cudaStream_t st)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    const int64_t rows = static_cast<int64_t>(L.max_q_len) * L.G;
-    if (rows <= 64)
-        return chunk::decode_launch(L, static_cast<int>(rows), min(sms, chunk::kMaxCtas), st);
-    k_chunk_rows<<<static_cast<unsigned>((L.tb.T * L.Hq + 7) / 8), 256, 0, st>>>(L);
-    return cudaGetLastError();
+    const int ctas = std::min(sms, chunk::kMaxCtas);
+    const int64_t rows = rows_of(L.Hq, L.Hkv, L.max_q_len);
+    return rows <= kFewRows ? chunk::decode_launch(L, static_cast<int>(rows), ctas, st) : chunk::tiles_launch(L, ctas, st);
 }
 
 } // namespace pw

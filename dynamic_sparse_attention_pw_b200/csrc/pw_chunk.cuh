@@ -33,6 +33,31 @@ constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr int kBlock = 128;    // keys per block
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
 
+using F2 = uint64_t; // two fp32, for the packed instructions
+
+__device__ __forceinline__ F2 pack2(float lo, float hi)
+{
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+
+__device__ __forceinline__ void unpack2(F2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 struct Sequence {
     int row0;     // first row of Q (token) of the sequence
     int qlen;     // new tokens
@@ -193,6 +218,7 @@ struct Job {
     int row, rows; // the tile's rows
     int b, h;
     int tok0;      // Q row of the sequence's first token
+    int ctx;       // its position
     int slot;      // -1: the whole tile, 0 / 1: partial
 };
 
@@ -280,7 +306,7 @@ struct Pieces {
             return false;
         const Tile t = tile_of<NT>(L, s, i);
         const int n = static_cast<int>(min(static_cast<int64_t>(t.nblk - off), x1 - x));
-        j = Job{n, t.blk0 + off, t.lo, t.hi, t.row, t.rows, b, h, s.row0, off > 0 ? 0 : (n < t.nblk ? 1 : -1)};
+        j = Job{n, t.blk0 + off, t.lo, t.hi, t.row, t.rows, b, h, s.row0, static_cast<int>(s.ctx), off > 0 ? 0 : (n < t.nblk ? 1 : -1)};
         x += n;
         off = 0;
         if (++i == tiles) {
@@ -309,7 +335,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-static __device__ __noinline__ bool wait_spin(uint64_t *bar, uint32_t parity, int32_t *abort_flag)
+static __device__ __forceinline__ bool wait_spin(uint64_t *bar, uint32_t parity, int32_t *abort_flag)
 {
     const long long t0 = clock64();
     for (;;) {
@@ -440,6 +466,8 @@ cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap 
 
 cudaError_t decode_launch(const ChunkLaunch &L, int rows, int ctas, cudaStream_t st);
 size_t decode_workspace(int rows);
+cudaError_t tiles_launch(const ChunkLaunch &L, int ctas, cudaStream_t st);
+size_t tiles_workspace();
 
 // Joins the partial results of the tiles that were cut: block j does the tile that stretch j starts
 // inside of, unless an earlier stretch starts inside of it too.  One warp per row.  Its blocks are

@@ -80,31 +80,6 @@ struct __align__(1024) DecSmem {
     int32_t abort_flag;
 };
 
-using F2 = uint64_t; // two fp32, for the packed instructions
-
-__device__ __forceinline__ F2 pack2(float lo, float hi)
-{
-    F2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-
-__device__ __forceinline__ void unpack2(F2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // One key's weights of two rows, 0..1, rounded to f16 and cut exactly into three E4M3 parts each, the
 // second and third times 2^4 and 2^8: bits 7..14 and 23..30 of w hold the codes of the two rows.
 __device__ __forceinline__ void split3(float p0, float p1, uint32_t (&w)[3])

@@ -1,0 +1,576 @@
+// pw_chunk_tiles.cu -- pw_chunk_attn for many rows: chunks of a prompt.
+//
+// A tile is 256 rows, two halves of 128, against blocks of 128 keys.  Per half and block
+//   S = q1 K^T + q2 K^T   (M = 128 rows, N = 128 keys; E4M3: K as stored, the query's exact parts)
+//   O += P V              (M = 128 rows, N = 128 dims, K = 128 keys; f16: P from TMEM, V converted)
+// The E4M3 products of the two query parts take as long as one bf16 product would and spare the
+// conversion of K; V is converted (exactly) to f16 once for both halves.  The halves alternate: while
+// one is in the softmax, the tensor cores work for the other.  The softmax is one thread a row: no
+// reduction crosses threads.
+//
+// A row's running maximum is a reference that moves when a score exceeds it by more than 2^8 (f16
+// holds up to 2^15); the block's weights are formed with the old reference, on the assumption that it
+// holds, and formed again when it did not.
+//
+//   warps 0-3    softmax, first half; the end of its rows
+//   warps 4-7    softmax, second half
+//   warps 8-11   the next tile's queries; V to f16
+//   warp 12      load: page ids, copies of K and V, job records
+//   warp 13      the products
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pw_chunk.cuh"
+
+namespace pw {
+namespace chunk {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 256;
+constexpr int kHalf = 128;
+constexpr int kJobs = 4;
+constexpr int kMinBlocks = 1;
+constexpr int kNK = 3, kNV = 2; // K and V stages
+constexpr float kRaise = 8.f;   // a row's reference moves when a score exceeds it by more (base 2)
+// Registers: softmax warps take what the others give up (256 x 168 + 256 x 80 <= 512 x 128).
+constexpr int kRegsSoftmax = 168, kRegsOther = 80;
+
+struct __align__(1024) TileSmem {
+    uint8_t q[2][2][kHalf * 128];   // [half][part][row][dim] E4M3
+    uint8_t k[kNK][kBlock * 128];   // E4M3, swizzled by the copy
+    uint8_t v[kNV][kBlock * 128];   // E4M3 as stored
+    uint8_t v16[2][2][kBlock * 128]; // [block % 2][dims 0-63, 64-127][key][dim] f16, swizzled
+    float c[2][2][kHalf];           // [half][its tile % 2]: factor of a row's scores
+    Job job[kJobs];
+    Plan plan;
+    uint64_t job_full[kJobs], job_empty[kJobs];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[kNK], k_empty[kNK], v_full[kNV], v_empty[kNV];
+    uint64_t v16_full[2], v16_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t drain;
+    uint32_t k_issued, v_issued; // blocks whose copies were issued
+    uint32_t tmem;
+    int32_t abort_flag;
+};
+static_assert(sizeof(TileSmem) + 1024 <= 227 * 1024, "shared-memory layout too large");
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ int halves(const Job &j) { return j.rows > kHalf ? 2 : 1; }
+
+// Sixteen E4M3 codes to f16.
+__device__ __forceinline__ void e4m3x16_to_f16(const uint4 x, uint4 &h0, uint4 &h1)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}\n"
+            : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+            : "r"(w[i]));
+    h0 = make_uint4(h[0], h[1], h[2], h[3]);
+    h1 = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_chunk_tiles(const ChunkLaunch L, const __grid_constant__ CUtensorMap map_k)
+{
+    constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 128);
+    constexpr uint32_t kIdescO = idesc_f16_f32(128, 128, false, true);
+    constexpr uint32_t kColS = 128, kColO = 256; // S / P of the halves at columns 0 and 128, O at 256 and 384
+    extern __shared__ uint8_t smem_raw[];
+    TileSmem &sm = *reinterpret_cast<TileSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+
+    if (tid == 0) {
+        for (int i = 0; i < kJobs; ++i) {
+            mbar_init(&sm.job_full[i], 1);
+            mbar_init(&sm.job_empty[i], 8 + 4 + 1); // softmax, query and product warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.v16_full[i], 4);
+            mbar_init(&sm.v16_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.o_free[i], 4);
+        }
+        for (int i = 0; i < kNK; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+        }
+        for (int i = 0; i < kNV; ++i) {
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 4);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.k_issued = sm.v_issued = 0;
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 13) {
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
+    }
+    make_plan<kRows>(L, sm.plan, cta, kMinBlocks);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    int32_t *const ab = &sm.abort_flag;
+
+    if (warp < 8) {
+        // ---------------- softmax ----------------
+        regs_inc<kRegsSoftmax>();
+        const int a = warp >> 2; // half
+        const int r = 128 * a + (tid & 127);
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t s_addr = tmem + lanes + a * kColS, o_addr = tmem + lanes + kColO + a * 128;
+        uint32_t nt = 0, ns = 0; // tiles and blocks of this half so far
+        for (uint32_t n = 0;; ++n) {
+            if (!warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab))
+                break;
+            const Job &j = sm.job[n % kJobs];
+            const int nblk = j.nblk, blk0 = j.blk0;
+            if (nblk < 0)
+                break;
+            if (a >= halves(j)) {
+                warp_arrive(&sm.job_empty[n % kJobs], lane);
+                continue;
+            }
+            const int last_pos = L.pm.max_pages * kPageTokens - 1;
+            auto pos_of = [&](int row) { return static_cast<int>(min(static_cast<int64_t>(j.ctx) + (j.row + row) / L.G, static_cast<int64_t>(last_pos))); };
+            const bool real = r < j.rows;
+            const int pos = real ? pos_of(r) : -1;
+            const int pos_lo = pos_of(128 * a), pos_hi = pos_of(min(j.rows, 128 * a + 128) - 1);
+            if (!warp_wait(&sm.q_full[a], nt & 1u, ab))
+                break;
+            const float c = sm.c[a][nt & 1u][r & 127];
+            const F2 cc = pack2(c, c);
+            float m = kNoMax, l = 0.f;
+            bool ok = true;
+            for (int k = 0; k < nblk; ++k, ++ns) {
+                ok = warp_wait(&sm.s_full[a], ns & 1u, ab);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const int b0 = (blk0 + k) * kBlock;
+                // some row does not see the whole block
+                const bool edge = b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window);
+                uint32_t p[2][32];
+                float lb;
+                for (;;) {
+                    const F2 nm = pack2(-m, -m);
+                    float top = -INFINITY;
+                    F2 sum[2] = {0ull, 0ull};
+                    uint32_t s[2][16];
+                    tmem_ld16(s_addr, s[0]);
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch) {
+                        uint32_t (&x)[16] = s[ch & 1];
+                        tmem_ld_wait16(x);
+                        if (ch < 7)
+                            tmem_ld16(s_addr + 16 * (ch + 1), s[(ch + 1) & 1]);
+                        if (edge) {
+                            const int d = pos - b0 - 16 * ch; // distance of the chunk's first key behind the token
+                            const int w = L.window > 0 ? L.window : 0x7FFFFFFF;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (d < e || d - e >= w)
+                                    x[e] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            top = fmaxf(fmaxf(top, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))),
+                                        fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float p0, p1;
+                            unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, nm), p0, p1);
+                            p0 = attn::ex2(p0);
+                            p1 = attn::ex2(p1);
+                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(p0, p1));
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[ch >> 2][8 * (ch & 3) + e / 2]) : "f"(p1), "f"(p0));
+                        }
+                    }
+                    float x0, x1;
+                    unpack2(add2(sum[0], sum[1]), x0, x1);
+                    lb = x0 + x1;
+                    const float y = top * c;
+                    const bool over = y > m + kRaise;
+                    if (!__any_sync(kFull, over))
+                        break;
+                    // The reference moves, what the row has so far is scaled (the products before this
+                    // block are complete: its S was issued after them), and the weights are formed again.
+                    const float mn = over ? y : m, alpha = attn::ex2(m - mn);
+                    l *= alpha;
+                    if (k > 0) {
+#pragma unroll 1
+                        for (int ch = 0; ch < 8; ++ch) {
+                            tmem_ld16(o_addr + 16 * ch, s[0]);
+                            tmem_ld_wait16(s[0]);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * alpha);
+                            tmem_st16(o_addr + 16 * ch, s[0]);
+                        }
+                    }
+                    m = mn;
+                }
+                l += lb;
+                tmem_st32(s_addr, p[0]);
+                tmem_st32(s_addr + 32, p[1]);
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(&sm.p_full[a], lane);
+            }
+            if (!ok || !warp_wait(&sm.o_full[a], nt & 1u, ab))
+                break;
+            tc_fence_after();
+            // ---- the end of the tile ----
+            float *const part = j.slot >= 0 ? partial<kRows>(L, cta, j.slot) : nullptr;
+            const int flat = j.row + r, tok = flat / L.G;
+            const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
+            const float inv = L.v_scale / l;
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + 32 * ch, o);
+                tmem_ld_wait(o);
+                if (real && part != nullptr) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(part + r * kHeadDim + 32 * ch);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else if (real) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    uint4 *dst = reinterpret_cast<uint4 *>(L.O + at * kHeadDim + 32 * ch);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                }
+            }
+            tc_fence_before();
+            warp_arrive(&sm.o_free[a], lane);
+            if (real && part != nullptr) {
+                part[kRows * kHeadDim + r] = m;
+                part[kRows * (kHeadDim + 1) + r] = l;
+            } else if (real && L.lse != nullptr) {
+                L.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+            }
+            warp_arrive(&sm.job_empty[n % kJobs], lane);
+            ++nt;
+        }
+    } else if (warp < 12) {
+        // ---------------- queries; V to f16 ----------------
+        regs_dec<kRegsOther>();
+        const int w = warp - 8, hl = lane >> 4, l16 = lane & 15, t = tid - 256;
+        uint32_t nt[2] = {0, 0}, c = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
+            if (!ok)
+                break;
+            const Job j = sm.job[n % kJobs];
+            warp_arrive(&sm.job_empty[n % kJobs], lane);
+            if (j.nblk < 0)
+                break;
+            for (int a = 0; ok && a < halves(j); ++a) {
+                ok = warp_wait(&sm.q_empty[a], (nt[a] & 1u) ^ 1u, ab);
+                if (!ok)
+                    break;
+                // sixteen lanes a row, four rows of a half-warp at a time
+#pragma unroll 1
+                for (int r0 = 2 * w + hl; r0 < kHalf; r0 += 32) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 128 * a + r0 + 8 * i, flat = j.row + r, tok = flat / L.G, head = j.h * L.G + flat - tok * L.G;
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < j.rows)
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
+                                                                         static_cast<int64_t>(head) * L.q_sh) + l16);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + 8 * i;
+                        const float f = stage_q_row(v[i], sm.q[a][0], r, kHalf + r, l16, L.score_scale);
+                        if (l16 == 0)
+                            sm.c[a][nt[a] & 1u][r] = f;
+                    }
+                }
+                fence_proxy_async_smem();
+                warp_arrive(&sm.q_full[a], lane);
+                ++nt[a];
+            }
+            for (int k = 0; ok && k < j.nblk; ++k, ++c) {
+                const uint32_t sv = c % kNV, slot = c & 1u;
+                ok = warp_wait(&sm.v_full[sv], (c / kNV) & 1u, ab) && warp_wait(&sm.v16_empty[slot], ((c >> 1) & 1u) ^ 1u, ab);
+                if (!ok)
+                    break;
+                // Values of keys that no row of the tile sees may be any bytes, NaN codes among them,
+                // and zero times NaN is not zero: they enter as zeros.
+                const int b0 = (j.blk0 + k) * kBlock;
+                const bool edge = b0 < j.lo || b0 + kBlock > j.hi;
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int q = t + 128 * i, key = q >> 3, c16 = q & 7;
+                    uint4 x = *reinterpret_cast<const uint4 *>(sm.v[sv] + key * 128 + c16 * 16);
+                    if (edge && (b0 + key < j.lo || b0 + key >= j.hi))
+                        x = make_uint4(0u, 0u, 0u, 0u);
+                    uint4 h0, h1;
+                    e4m3x16_to_f16(x, h0, h1);
+                    uint8_t *const dst = sm.v16[slot][c16 >> 2];
+                    const int j0 = (2 * c16) & 7;
+                    // half of the threads store in the other order, so that eight of them meet all banks
+                    const bool flip = c16 >= 4;
+                    *reinterpret_cast<uint4 *>(dst + attn::swz(key, j0 + flip)) = flip ? h1 : h0;
+                    *reinterpret_cast<uint4 *>(dst + attn::swz(key, j0 + 1 - flip)) = flip ? h0 : h1;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.v16_full[slot]);
+                    mbar_arrive(&sm.v_empty[sv]);
+                }
+            }
+        }
+    } else {
+        regs_dec<kRegsOther>();
+        if (warp == 12) {
+            // ---------------- load ----------------
+            Pieces<kRows> pieces;
+            pieces.begin(L, sm.plan, reinterpret_cast<Cut *>(L.workspace), cta, lane);
+            auto fetch = [&](const Job &j, int k) { // slots of the 32 pages of job j from block k on, one a lane
+                const int pg = 2 * (j.blk0 + k) + lane; // between the pages that hold a key of the tile
+                return pg >= (j.lo >> 6) && pg <= ((j.hi - 1) >> 6) && pg < 2 * (j.blk0 + j.nblk) ? phys_slot(L, j.b, pg) : -1;
+            };
+            uint32_t c = 0;
+            Job j;
+            bool more = pieces.next(L, j), ok = true;
+            int ids = more ? fetch(j, 0) : -1;
+            for (uint32_t n = 0; ok; ++n) {
+                ok = warp_wait(&sm.job_empty[n % kJobs], ((n / kJobs) & 1u) ^ 1u, ab);
+                if (!ok)
+                    break;
+                if (!more)
+                    j.nblk = -1;
+                if (lane == 0) {
+                    sm.job[n % kJobs] = j;
+                    mbar_arrive(&sm.job_full[n % kJobs]);
+                }
+                if (!more)
+                    break;
+                Job jn;
+                int ids_n = -1, nxt = j.nblk > 16 ? fetch(j, 16) : -1;
+                // the next job is formed, and its first page ids asked for, while copies are in flight
+                const int ahead = min(j.nblk, kNV) - 1;
+                for (int k = 0; k < j.nblk; ++k, ++c) {
+                    if (k > 0 && (k & 15) == 0) {
+                        ids = nxt;
+                        if (k + 16 < j.nblk)
+                            nxt = fetch(j, k + 16);
+                    }
+                    const int s0 = __shfl_sync(kFull, ids, 2 * (k & 15)), s1 = __shfl_sync(kFull, ids, 2 * (k & 15) + 1);
+                    const uint32_t bytes = ((s0 >= 0) + (s1 >= 0)) * attn::kPageBytes;
+                    const int y0 = (s0 * L.Hkv + j.h) * kPageTokens, y1 = (s1 * L.Hkv + j.h) * kPageTokens;
+                    const uint32_t sk = c % kNK, sv = c % kNV;
+                    ok = warp_wait(&sm.k_empty[sk], ((c / kNK) & 1u) ^ 1u, ab);
+                    if (!ok)
+                        break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sm.k_full[sk], bytes);
+                        if (s0 >= 0)
+                            tma_load_2d(sm.k[sk], &map_k, 0, y0, &sm.k_full[sk]);
+                        if (s1 >= 0)
+                            tma_load_2d(sm.k[sk] + attn::kPageBytes, &map_k, 0, y1, &sm.k_full[sk]);
+                        sm.k_issued = c + 1;
+                    }
+                    __syncwarp();
+                    ok = warp_wait(&sm.v_empty[sv], ((c / kNV) & 1u) ^ 1u, ab);
+                    if (!ok)
+                        break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sm.v_full[sv], bytes);
+                        if (s0 >= 0)
+                            bulk_g2s(sm.v[sv], L.V + static_cast<int64_t>(y0) * kHeadDim, attn::kPageBytes, &sm.v_full[sv]);
+                        if (s1 >= 0)
+                            bulk_g2s(sm.v[sv] + attn::kPageBytes, L.V + static_cast<int64_t>(y1) * kHeadDim, attn::kPageBytes, &sm.v_full[sv]);
+                        sm.v_issued = c + 1;
+                    }
+                    __syncwarp();
+                    if (k == ahead) {
+                        more = pieces.next(L, jn);
+                        if (more)
+                            ids_n = fetch(jn, 0);
+                    }
+                }
+                j = jn;
+                ids = ids_n;
+            }
+        } else if (warp == 13) {
+            // ---------------- products ----------------
+            // Of each half in turn: the products of the block before, then S of this one.  The P of a
+            // block lies over the S it came from; the tensor core takes its work in order, so S of the
+            // next block may follow the products that read P without a wait.
+            const uint64_t dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024), dq = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+            const uint64_t dv = sdesc_sw128(smem_u32(sm.v16[0][0]), kBlock * 128, 1024);
+            uint32_t c = 0, ns[2] = {0, 0}, nt[2] = {0, 0}; // blocks; products and tiles of each half
+            bool ok = true;
+            int pend = 0;                        // halves of block c - 1 whose products are still to come
+            bool p_first = false, p_last = false; // that block is the first, the last of its tile
+            auto products = [&](int a) {
+                const uint32_t slot = (c - 1) & 1u;
+                if (!warp_wait(&sm.p_full[a], ns[a] & 1u, ab) || !warp_wait(&sm.v16_full[slot], ((c - 1) >> 1) & 1u, ab) ||
+                    (p_first && !warp_wait(&sm.o_free[a], (nt[a] & 1u) ^ 1u, ab)))
+                    return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_f16_ts(tmem + kColO + a * 128, tmem + a * kColS + 8 * kk, dv + ((slot * 2 * kBlock * 128 + kk * 2048) >> 4),
+                                   kIdescO, kk > 0 || !p_first);
+                    if (p_last)
+                        mma_commit(&sm.o_full[a]);
+                    if (a == pend - 1)
+                        mma_commit(&sm.v16_empty[slot]);
+                }
+                __syncwarp();
+                ++ns[a];
+                nt[a] += p_last;
+                return true;
+            };
+            uint32_t nq[2] = {0, 0};
+            for (uint32_t n = 0; ok; ++n) {
+                ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
+                if (!ok)
+                    break;
+                const Job &job = sm.job[n % kJobs];
+                const int nblk = job.nblk, hv = halves(job);
+                warp_arrive(&sm.job_empty[n % kJobs], lane);
+                // the last products of the tile before
+                for (int a = 0; ok && a < pend; ++a)
+                    ok = products(a);
+                pend = 0;
+                if (nblk < 0)
+                    break;
+                for (int k = 0; ok && k < nblk; ++k) {
+                    const uint32_t sk = c % kNK;
+                    for (int a = 0; a < hv; ++a) {
+                        if (k > 0) {
+                            ok = products(a);
+                            if (!ok)
+                                break;
+                        } else {
+                            ok = warp_wait(&sm.q_full[a], nq[a] & 1u, ab);
+                            if (!ok)
+                                break;
+                            ++nq[a];
+                        }
+                        if (a == 0) {
+                            ok = warp_wait(&sm.k_full[sk], (c / kNK) & 1u, ab);
+                            if (!ok)
+                                break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) // four steps of each query part
+                                mma_f8_ss(tmem + a * kColS, dq + ((a * 2 * kHalf * 128 + (kk >> 2) * kHalf * 128 + (kk & 3) * 32) >> 4),
+                                          dk + ((sk * kBlock * 128 + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
+                            mma_commit(&sm.s_full[a]);
+                            if (k == nblk - 1)
+                                mma_commit(&sm.q_empty[a]);
+                            if (a == hv - 1)
+                                mma_commit(&sm.k_empty[sk]);
+                        }
+                        __syncwarp();
+                    }
+                    ++c;
+                    pend = hv;
+                    p_first = k == 0;
+                    p_last = k == nblk - 1;
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (sm.abort_flag != 0) {
+        // Copies and products in flight land before the CTA leaves (bounded waits).
+        if (tid == 0) {
+            set_status(L.status, PW_ERR_TIMEOUT);
+            const uint32_t nk = sm.k_issued, nv = sm.v_issued;
+            for (uint32_t s = 0; s < kNK && s < nk; ++s)
+                (void)mbar_wait(&sm.k_full[s], ((nk - 1 - s) / kNK) & 1u);
+            for (uint32_t s = 0; s < kNV && s < nv; ++s)
+                (void)mbar_wait(&sm.v_full[s], ((nv - 1 - s) / kNV) & 1u);
+        }
+        if (warp == 13) {
+            if (elect_one()) {
+                mma_commit(&sm.drain);
+                (void)mbar_wait(&sm.drain, 0);
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+} // namespace
+
+size_t tiles_workspace() { return workspace_bytes<kRows>(); }
+
+cudaError_t tiles_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
+{
+    CUtensorMap k;
+    cudaError_t e = page_tensor(L.K, L, &k);
+    const int smem = static_cast<int>(sizeof(TileSmem) + 1024);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_chunk_tiles, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    k_chunk_tiles<<<ctas, kThreads, smem, st>>>(L, k);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? merge_launch<kRows>(L, ctas, st) : e;
+}
+
+} // namespace chunk
+} // namespace pw
