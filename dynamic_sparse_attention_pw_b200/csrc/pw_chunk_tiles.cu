@@ -8,9 +8,9 @@
 // one is in the softmax, the tensor cores work for the other.  The softmax is one thread a row: no
 // reduction crosses threads.
 //
-// A row's running maximum is a reference that moves when a score exceeds it by more than 2^8 (f16
-// holds up to 2^15); the block's weights are formed with the old reference, on the assumption that it
-// holds, and formed again when it did not.
+// A row's running maximum is a reference, a whole number, that moves when a score of a chunk of 32
+// keys exceeds it by more than 2^8 (f16 holds up to 2^15); what the row has so far, the weights of the
+// block's earlier chunks among it, is then scaled by a power of two.
 //
 //   warps 0-3    softmax, first half; the end of its rows
 //   warps 4-7    softmax, second half
@@ -36,8 +36,6 @@ constexpr int kJobs = 4;
 constexpr int kMinBlocks = 1;
 constexpr int kNK = 3, kNV = 2; // K and V stages
 constexpr float kRaise = 8.f;   // a row's reference moves when a score exceeds it by more (base 2)
-// Registers: softmax warps take what the others give up (256 x 168 + 256 x 80 <= 512 x 128).
-constexpr int kRegsSoftmax = 168, kRegsOther = 80;
 
 struct __align__(1024) TileSmem {
     uint8_t q[2][2][kHalf * 128];   // [half][part][row][dim] E4M3
@@ -68,11 +66,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
                  : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
 {
     F2 d;
@@ -95,6 +88,39 @@ __device__ __forceinline__ void e4m3x16_to_f16(const uint4 x, uint4 &h0, uint4 &
             : "r"(w[i]));
     h0 = make_uint4(h[0], h[1], h[2], h[3]);
     h1 = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&x)[32])
+{
+    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = fmaxf(t[i], fmaxf(__uint_as_float(x[e + 2 * i]), __uint_as_float(x[e + 2 * i + 1])));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// A thread's row times alpha, a power of two: no pieces of 16 dims of its accumulator, and np pieces
+// of 32 weights.  The products issued so far are complete: the scores at hand were issued after them.
+static __device__ __noinline__ void rescale(uint32_t o_addr, int no, uint32_t p_addr, int np, float alpha)
+{
+    tmem_st_wait();
+    const __half2 h = __float2half2_rn(alpha);
+#pragma unroll 1
+    for (int i = 0; i < no + np; ++i) {
+        const uint32_t at = i < no ? o_addr + 16 * i : p_addr + 16 * (i - no);
+        uint32_t x[16];
+        tmem_ld16(at, x);
+        tmem_ld_wait16(x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const __half2 w = __hmul2(*reinterpret_cast<const __half2 *>(&x[e]), h);
+            x[e] = i < no ? __float_as_uint(__uint_as_float(x[e]) * alpha) : *reinterpret_cast<const uint32_t *>(&w);
+        }
+        tmem_st16(at, x);
+    }
+    tmem_st_wait();
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -148,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ---------------- softmax ----------------
-        regs_inc<kRegsSoftmax>();
         const int a = warp >> 2; // half
         const int r = 128 * a + (tid & 127);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -174,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             const float c = sm.c[a][nt & 1u][r & 127];
             const F2 cc = pack2(c, c);
-            float m = kNoMax, l = 0.f;
+            float m = kNoMax;
+            F2 l[2] = {0ull, 0ull};
             bool ok = true;
             for (int k = 0; k < nblk; ++k, ++ns) {
                 ok = warp_wait(&sm.s_full[a], ns & 1u, ab);
@@ -182,71 +208,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 tc_fence_after();
                 const int b0 = (blk0 + k) * kBlock;
-                // some row does not see the whole block
-                const bool edge = b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window);
-                uint32_t p[2][32];
-                float lb;
-                for (;;) {
-                    const F2 nm = pack2(-m, -m);
-                    float top = -INFINITY;
-                    F2 sum[2] = {0ull, 0ull};
-                    uint32_t s[2][16];
-                    tmem_ld16(s_addr, s[0]);
-#pragma unroll
-                    for (int ch = 0; ch < 8; ++ch) {
-                        uint32_t (&x)[16] = s[ch & 1];
-                        tmem_ld_wait16(x);
-                        if (ch < 7)
-                            tmem_ld16(s_addr + 16 * (ch + 1), s[(ch + 1) & 1]);
-                        if (edge) {
-                            const int d = pos - b0 - 16 * ch; // distance of the chunk's first key behind the token
-                            const int w = L.window > 0 ? L.window : 0x7FFFFFFF;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (d < e || d - e >= w)
-                                    x[e] = 0xFF800000u;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            top = fmaxf(fmaxf(top, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))),
-                                        fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float p0, p1;
-                            unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, nm), p0, p1);
-                            p0 = attn::ex2(p0);
-                            p1 = attn::ex2(p1);
-                            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(p0, p1));
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[ch >> 2][8 * (ch & 3) + e / 2]) : "f"(p1), "f"(p0));
-                        }
-                    }
-                    float x0, x1;
-                    unpack2(add2(sum[0], sum[1]), x0, x1);
-                    lb = x0 + x1;
-                    const float y = top * c;
-                    const bool over = y > m + kRaise;
-                    if (!__any_sync(kFull, over))
-                        break;
-                    // The reference moves, what the row has so far is scaled (the products before this
-                    // block are complete: its S was issued after them), and the weights are formed again.
-                    const float mn = over ? y : m, alpha = attn::ex2(m - mn);
-                    l *= alpha;
-                    if (k > 0) {
+                // Where some row does not see the whole block, the scores are masked in place first, which
+                // keeps the masks out of every other block.
+                if (b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window)) {
+                    const int w = L.window > 0 ? L.window : 0x7FFFFFFF;
 #pragma unroll 1
-                        for (int ch = 0; ch < 8; ++ch) {
-                            tmem_ld16(o_addr + 16 * ch, s[0]);
-                            tmem_ld_wait16(s[0]);
+                    for (int ch = 0; ch < 4; ++ch) {
+                        const int d = pos - b0 - 32 * ch; // distance of the chunk's first key behind the token
+                        uint32_t x[32];
+                        tmem_ld32(s_addr + 32 * ch, x);
+                        tmem_ld_wait(x);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * alpha);
-                            tmem_st16(o_addr + 16 * ch, s[0]);
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (d < e || d - e >= w)
+                                x[e] = 0xFF800000u;
+                        tmem_st32(s_addr + 32 * ch, x);
                     }
-                    m = mn;
+                    tmem_st_wait();
                 }
-                l += lb;
-                tmem_st32(s_addr, p[0]);
-                tmem_st32(s_addr + 32, p[1]);
+                uint32_t s[2][32]; // a chunk's scores arrive during the weights of the one before
+                tmem_ld32(s_addr, s[0]);
+                tmem_ld_wait(s[0]);
+                float y = max32(s[0]) * c;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t (&x)[32] = s[ch & 1], (&next)[32] = s[(ch + 1) & 1];
+                    if (ch < 3)
+                        tmem_ld32(s_addr + 32 * (ch + 1), next);
+                    if (__any_sync(kFull, y > m + kRaise)) {
+                        const float mn = y > m + kRaise ? ceilf(y) : m, alpha = attn::ex2(m - mn);
+                        m = mn;
+                        l[0] = mul2(l[0], pack2(alpha, alpha));
+                        l[1] = mul2(l[1], pack2(alpha, alpha));
+                        rescale(o_addr, k > 0 ? 8 : 0, s_addr, ch, alpha);
+                    }
+                    const F2 nm = pack2(-m, -m);
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0, p1;
+                        unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, nm), p0, p1);
+                        p0 = attn::ex2(p0);
+                        p1 = attn::ex2(p1);
+                        l[(e >> 1) & 1] = add2(l[(e >> 1) & 1], pack2(p0, p1));
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[e / 2]) : "f"(p1), "f"(p0));
+                    }
+                    tmem_st16(s_addr + 16 * ch, p); // over scores that have been read
+                    if (ch < 3) {
+                        tmem_ld_wait(next);
+                        y = max32(next) * c;
+                    }
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(&sm.p_full[a], lane);
@@ -258,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *const part = j.slot >= 0 ? partial<kRows>(L, cta, j.slot) : nullptr;
             const int flat = j.row + r, tok = flat / L.G;
             const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
-            const float inv = L.v_scale / l;
+            float l0, l1;
+            unpack2(add2(l[0], l[1]), l0, l1);
+            const float sum = l0 + l1, inv = L.v_scale / sum;
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t o[32];
@@ -286,16 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_arrive(&sm.o_free[a], lane);
             if (real && part != nullptr) {
                 part[kRows * kHeadDim + r] = m;
-                part[kRows * (kHeadDim + 1) + r] = l;
+                part[kRows * (kHeadDim + 1) + r] = sum;
             } else if (real && L.lse != nullptr) {
-                L.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+                L.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
             }
             warp_arrive(&sm.job_empty[n % kJobs], lane);
             ++nt;
         }
     } else if (warp < 12) {
         // ---------------- queries; V to f16 ----------------
-        regs_dec<kRegsOther>();
         const int w = warp - 8, hl = lane >> 4, l16 = lane & 15, t = tid - 256;
         uint32_t nt[2] = {0, 0}, c = 0;
         bool ok = true;
@@ -368,7 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        regs_dec<kRegsOther>();
         if (warp == 12) {
             // ---------------- load ----------------
             Pieces<kRows> pieces;
