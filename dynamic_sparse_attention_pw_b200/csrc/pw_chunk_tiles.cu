@@ -246,6 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
+                        if (e == 16 && ch < 3) { // the next chunk's maximum is found among these exponentials
+                            tmem_ld_wait(next);
+                            y = max32(next) * c;
+                        }
                         float p0, p1;
                         unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, nm), p0, p1);
                         p0 = attn::ex2(p0);
@@ -254,10 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[e / 2]) : "f"(p1), "f"(p0));
                     }
                     tmem_st16(s_addr + 16 * ch, p); // over scores that have been read
-                    if (ch < 3) {
-                        tmem_ld_wait(next);
-                        y = max32(next) * c;
-                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -465,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool p_first = false, p_last = false; // that block is the first, the last of its tile
             auto products = [&](int a) {
                 const uint32_t slot = (c - 1) & 1u;
-                if (!warp_wait(&sm.p_full[a], ns[a] & 1u, ab) || !warp_wait(&sm.v16_full[slot], ((c - 1) >> 1) & 1u, ab) ||
-                    (p_first && !warp_wait(&sm.o_free[a], (nt[a] & 1u) ^ 1u, ab)))
+                if (!warp_wait(&sm.v16_full[slot], ((c - 1) >> 1) & 1u, ab) ||
+                    (p_first && !warp_wait(&sm.o_free[a], (nt[a] & 1u) ^ 1u, ab)) || !warp_wait(&sm.p_full[a], ns[a] & 1u, ab))
                     return false;
                 tc_fence_after();
                 if (elect_one()) {
@@ -500,22 +500,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 for (int k = 0; ok && k < nblk; ++k) {
                     const uint32_t sk = c % kNK;
-                    for (int a = 0; a < hv; ++a) {
-                        if (k > 0) {
+                    ok = warp_wait(&sm.k_full[sk], (c / kNK) & 1u, ab);
+                    for (int a = 0; ok && a < hv; ++a) {
+                        if (k > 0)
                             ok = products(a);
-                            if (!ok)
-                                break;
-                        } else {
-                            ok = warp_wait(&sm.q_full[a], nq[a] & 1u, ab);
-                            if (!ok)
-                                break;
-                            ++nq[a];
-                        }
-                        if (a == 0) {
-                            ok = warp_wait(&sm.k_full[sk], (c / kNK) & 1u, ab);
-                            if (!ok)
-                                break;
-                        }
+                        else
+                            ok = warp_wait(&sm.q_full[a], nq[a]++ & 1u, ab);
+                        if (!ok)
+                            break;
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
