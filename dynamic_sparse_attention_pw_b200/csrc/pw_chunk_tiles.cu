@@ -49,7 +49,7 @@ struct __align__(1024) TileSmem {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kNK], k_empty[kNK], v_full[kNV], v_empty[kNV];
     uint64_t v16_full[2], v16_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_most[2], p_full[2], o_full[2], o_free[2]; // p_most: all weights of a block but the last 32 keys'
     uint64_t drain;
     uint32_t k_issued, v_issued; // blocks whose copies were issued
     uint32_t tmem;
@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.v16_full[i], 4);
             mbar_init(&sm.v16_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_most[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_full[i], 1);
             mbar_init(&sm.o_free[i], 4);
@@ -230,12 +231,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(s_addr, s[0]);
                 tmem_ld_wait(s[0]);
                 float y = max32(s[0]) * c;
+                bool any = __any_sync(kFull, y > m + kRaise);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     uint32_t (&x)[32] = s[ch & 1], (&next)[32] = s[(ch + 1) & 1];
                     if (ch < 3)
                         tmem_ld32(s_addr + 32 * (ch + 1), next);
-                    if (__any_sync(kFull, y > m + kRaise)) {
+                    if (any) {
                         const float mn = y > m + kRaise ? ceilf(y) : m, alpha = attn::ex2(m - mn);
                         m = mn;
                         l[0] = mul2(l[0], pack2(alpha, alpha));
@@ -246,9 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
+                        if (e == 4 && ch == 3) {
+                            tmem_st_wait();
+                            tc_fence_before();
+                            warp_arrive(&sm.p_most[a], lane);
+                        }
                         if (e == 16 && ch < 3) { // the next chunk's maximum is found among these exponentials
                             tmem_ld_wait(next);
                             y = max32(next) * c;
+                            any = __any_sync(kFull, y > m + kRaise);
                         }
                         float p0, p1;
                         unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, nm), p0, p1);
@@ -454,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 13) {
             // ---------------- products ----------------
-            // Of each half in turn: the products of the block before, then S of this one.  The P of a
+            // Of each half in turn: the products of the block before, begun when three quarters of its weights
+            // are there (the wake-up and six of eight steps pass during the rest), then S of this one.  The P of a
             // block lies over the S it came from; the tensor core takes its work in order, so S of the
             // next block may follow the products that read P without a wait.
             const uint64_t dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024), dq = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
@@ -466,14 +475,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto products = [&](int a) {
                 const uint32_t slot = (c - 1) & 1u;
                 if (!warp_wait(&sm.v16_full[slot], ((c - 1) >> 1) & 1u, ab) ||
-                    (p_first && !warp_wait(&sm.o_free[a], (nt[a] & 1u) ^ 1u, ab)) || !warp_wait(&sm.p_full[a], ns[a] & 1u, ab))
+                    (p_first && !warp_wait(&sm.o_free[a], (nt[a] & 1u) ^ 1u, ab)) || !warp_wait(&sm.p_most[a], ns[a] & 1u, ab))
+                    return false;
+                tc_fence_after();
+                const uint32_t o = tmem + kColO + a * 128, p = tmem + a * kColS;
+                const uint64_t v = dv + ((slot * 2 * kBlock * 128) >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 6; ++kk)
+                        mma_f16_ts(o, p + 8 * kk, v + 128 * kk, kIdescO, kk > 0 || !p_first);
+                }
+                __syncwarp();
+                if (!warp_wait(&sm.p_full[a], ns[a] & 1u, ab))
                     return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_f16_ts(tmem + kColO + a * 128, tmem + a * kColS + 8 * kk, dv + ((slot * 2 * kBlock * 128 + kk * 2048) >> 4),
-                                   kIdescO, kk > 0 || !p_first);
+                    for (int kk = 6; kk < 8; ++kk)
+                        mma_f16_ts(o, p + 8 * kk, v + 128 * kk, kIdescO, 1);
                     if (p_last)
                         mma_commit(&sm.o_full[a]);
                     if (a == pend - 1)
