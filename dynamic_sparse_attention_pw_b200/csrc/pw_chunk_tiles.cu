@@ -9,7 +9,7 @@
 // reduction crosses threads.
 //
 // A row's running maximum is a reference, a whole number, that moves when a score of a chunk of 32
-// keys exceeds it by more than 2^8 (f16 holds up to 2^15); what the row has so far, the weights of the
+// keys exceeds it by more than 2^15 (f16 ends at 2^16); what the row has so far, the weights of the
 // block's earlier chunks among it, is then scaled by a power of two.
 //
 //   warps 0-3    softmax, first half; the end of its rows
@@ -35,7 +35,7 @@ constexpr int kHalf = 128;
 constexpr int kJobs = 4;
 constexpr int kMinBlocks = 1;
 constexpr int kNK = 3, kNV = 2; // K and V stages
-constexpr float kRaise = 8.f;   // a row's reference moves when a score exceeds it by more (base 2)
+constexpr float kRaise = 15.f;  // a row's reference moves when a score exceeds it by more (base 2); f16 ends at 2^16
 
 struct __align__(1024) TileSmem {
     uint8_t q[2][2][kHalf * 128];   // [half][part][row][dim] E4M3
@@ -106,7 +106,6 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32])
 static __device__ __noinline__ void rescale(uint32_t o_addr, int no, uint32_t p_addr, int np, float alpha)
 {
     tmem_st_wait();
-    const __half2 h = __float2half2_rn(alpha);
 #pragma unroll 1
     for (int i = 0; i < no + np; ++i) {
         const uint32_t at = i < no ? o_addr + 16 * i : p_addr + 16 * (i - no);
@@ -115,7 +114,8 @@ static __device__ __noinline__ void rescale(uint32_t o_addr, int no, uint32_t p_
         tmem_ld_wait16(x);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const __half2 w = __hmul2(*reinterpret_cast<const __half2 *>(&x[e]), h);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[e]));
+            const __half2 w = __floats2half2_rn(f.x * alpha, f.y * alpha); // alpha itself may lie below f16's range
             x[e] = i < no ? __float_as_uint(__uint_as_float(x[e]) * alpha) : *reinterpret_cast<const uint32_t *>(&w);
         }
         tmem_st16(at, x);
@@ -235,8 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     uint32_t (&x)[32] = s[ch & 1], (&next)[32] = s[(ch + 1) & 1];
-                    if (ch < 3)
-                        tmem_ld32(s_addr + 32 * (ch + 1), next);
                     if (any) {
                         const float mn = y > m + kRaise ? ceilf(y) : m, alpha = attn::ex2(m - mn);
                         m = mn;
@@ -244,6 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l[1] = mul2(l[1], pack2(alpha, alpha));
                         rescale(o_addr, k > 0 ? 8 : 0, s_addr, ch, alpha);
                     }
+                    if (ch < 3) // behind the call, which must not find a load on its way into registers
+                        tmem_ld32(s_addr + 32 * (ch + 1), next);
                     const F2 nm = pack2(-m, -m);
                     uint32_t p[16];
 #pragma unroll
