@@ -83,6 +83,13 @@ __device__ __forceinline__ Sequence sequence(const ChunkLaunch &L, int b)
     return s;
 }
 
+// Token of a flat row: row / G.
+__device__ __forceinline__ int token_of(const ChunkLaunch &L, int row)
+{
+    const uint32_t n = static_cast<uint32_t>(row);
+    return static_cast<int>((__umulhi(n, L.g_mul) + n) >> L.g_shift);
+}
+
 struct Tile {
     int row, rows;  // flat rows of the sequence and kv head
     int lo, hi;     // keys [lo, hi) that some row of it sees
@@ -100,8 +107,8 @@ __device__ __forceinline__ Tile tile_of(const ChunkLaunch &L, const Sequence &s,
     Tile t;
     t.row = i * NT;
     t.rows = min(s.qlen * L.G - t.row, NT);
-    t.hi = position(s, (t.row + t.rows - 1) / L.G) + 1;
-    t.lo = L.window > 0 ? max(position(s, t.row / L.G) - L.window + 1, 0) : 0;
+    t.hi = position(s, token_of(L, t.row + t.rows - 1)) + 1;
+    t.lo = L.window > 0 ? max(position(s, token_of(L, t.row)) - L.window + 1, 0) : 0;
     t.blk0 = t.lo / kBlock;
     t.nblk = (t.hi + kBlock - 1) / kBlock - t.blk0;
     return t;
@@ -113,14 +120,32 @@ __device__ __forceinline__ int tiles_of(const ChunkLaunch &L, const Sequence &s)
     return (s.qlen * L.G + NT - 1) / NT;
 }
 
-// Blocks of one kv head of sequence b.
+// Blocks of one kv head of the sequences b of a warp's lanes (b >= B: 0).  A lane counts a few tiles by
+// itself, the warp those of a sequence of many together.
 template <int NT>
 __device__ __forceinline__ int64_t head_blocks(const ChunkLaunch &L, int b)
 {
-    const Sequence s = sequence(L, b);
+    constexpr int kAlone = 4;
+    const int lane = threadIdx.x & 31;
+    const Sequence s = b < L.tb.B ? sequence(L, b) : Sequence{0, 0, 0, 0};
+    const int tiles = tiles_of<NT>(L, s);
     int64_t n = 0;
-    for (int i = 0, e = tiles_of<NT>(L, s); i < e; ++i)
-        n += tile_of<NT>(L, s, i).nblk;
+    if (tiles <= kAlone)
+        for (int i = 0; i < tiles; ++i)
+            n += tile_of<NT>(L, s, i).nblk;
+    for (uint32_t many = __ballot_sync(kFull, tiles > kAlone); many != 0u; many &= many - 1) {
+        const int from = __ffs(many) - 1;
+        const Sequence o{__shfl_sync(kFull, s.row0, from), __shfl_sync(kFull, s.qlen, from), __shfl_sync(kFull, s.ctx, from),
+                         __shfl_sync(kFull, s.last, from)};
+        int64_t m = 0;
+        for (int i = lane, e = __shfl_sync(kFull, tiles, from); i < e; i += 32)
+            m += tile_of<NT>(L, o, i).nblk;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            m += __shfl_xor_sync(kFull, m, d);
+        if (lane == from)
+            n = m;
+    }
     return n;
 }
 
@@ -171,10 +196,10 @@ template <int NT>
 __device__ void make_plan(const ChunkLaunch &L, Plan &p, int cta, int min_blocks)
 {
     const int nt = blockDim.x, tid = threadIdx.x, B = L.tb.B;
-    int64_t mine = tid < B ? head_blocks<NT>(L, tid) : 0, total = 0;
+    int64_t mine = head_blocks<NT>(L, tid), total = 0;
     int64_t all = mine;
-    for (int b = tid + nt; b < B; b += nt)
-        all += head_blocks<NT>(L, b);
+    for (int b = nt; b < B; b += nt)
+        all += head_blocks<NT>(L, b + tid);
     (void)block_scan(all, p.scan, total);
     total *= L.Hkv;
     const int ctas = static_cast<int>(max(min(static_cast<int64_t>(gridDim.x), total / min_blocks), static_cast<int64_t>(1)));
@@ -194,7 +219,7 @@ __device__ void make_plan(const ChunkLaunch &L, Plan &p, int cta, int min_blocks
         for (int base = 0; base < B; base += nt) {
             const int b = base + tid;
             if (base > 0)
-                mine = b < B ? head_blocks<NT>(L, b) : 0;
+                mine = head_blocks<NT>(L, b);
             int64_t sum;
             const int64_t incl = run + block_scan(mine, p.scan, sum) * L.Hkv;
             if (mine > 0 && incl - mine * L.Hkv <= x0 && x0 < incl) {
@@ -429,9 +454,16 @@ __device__ __forceinline__ void split_q8(const uint4 v, float scale, uint2 &q1, 
     q2 = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
 }
 
+// The factor that takes the score of a row's parts to a base-2 exponent, from the row's largest
+// exponent; NaN for a row that holds an infinity or NaN, so that its output is NaN.  Kept above zero, so
+// that a masked score (-infinity) stays one in a row of zeros.
+__device__ __forceinline__ float q_factor(uint32_t e, float score_scale)
+{
+    return e == 255u ? __int_as_float(0x7FC00000) : fmaxf(score_scale * exp2i(-q_exp(e)), 1e-30f);
+}
+
 // Sixteen lanes of a half-warp (l = lane % 16) bring one row: its two parts into rows r1 and r2 of a
-// K-major operand tile (128-byte rows, 128-byte swizzle).  Returns the factor that takes the parts'
-// score to a base-2 exponent; NaN for a row that holds an infinity or NaN, so that its output is NaN.
+// K-major operand tile (128-byte rows, 128-byte swizzle).  Returns the row's factor.
 // v: the lane's eight elements.
 __device__ __forceinline__ float stage_q_row(const uint4 v, uint8_t *tile, int r1, int r2, int l, float score_scale)
 {
@@ -445,8 +477,7 @@ __device__ __forceinline__ float stage_q_row(const uint4 v, uint8_t *tile, int r
     const int in = (l & 1) * 8;
     *reinterpret_cast<uint2 *>(tile + attn::swz(r1, l >> 1) + in) = q1;
     *reinterpret_cast<uint2 *>(tile + attn::swz(r2, l >> 1) + in) = q2;
-    // kept above zero, so that a masked score (-infinity) stays one in a row of zeros
-    return e == 255u ? __int_as_float(0x7FC00000) : fmaxf(score_scale * exp2i(-s), 1e-30f);
+    return q_factor(e, score_scale);
 }
 
 // Physical slot of a page, checked; 0 where the entry is bad (recorded).
@@ -470,59 +501,81 @@ cudaError_t tiles_launch(const ChunkLaunch &L, int ctas, cudaStream_t st);
 size_t tiles_workspace();
 
 // Joins the partial results of the tiles that were cut: block j does the tile that stretch j starts
-// inside of, unless an earlier stretch starts inside of it too.  One warp per row.  Its blocks are
-// brought up while the attention kernel still runs (programmatic launch; 128 threads of 32
-// registers fit beside it) and wait for its end.
+// inside of, unless an earlier stretch starts inside of it too.  A warp has NT / 64 rows (one of a
+// small tile).  Where the attention kernel leaves registers (few rows), the blocks are brought up while
+// it still runs (programmatic launch) and wait for its end: 128 threads of 32 registers fit beside it.
 template <int NT>
-__global__ void __launch_bounds__(128, 16) k_chunk_merge(const ChunkLaunch L)
+__global__ void __launch_bounds__(128, NT <= 32 ? 16 : 8) k_chunk_merge(const ChunkLaunch L)
 {
+    constexpr int kR = NT <= 64 ? 1 : NT / 64;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int j = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int j = blockIdx.x, lane = threadIdx.x & 31, r0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * kR;
     const Cut c = reinterpret_cast<const Cut *>(L.workspace)[j];
-    if (!c.inside || r >= c.rows || stretch(c.total, c.ctas, j - 1) > c.ts)
+    if (!c.inside || r0 >= c.rows || stretch(c.total, c.ctas, j - 1) > c.ts)
         return;
     int n = 1; // pieces: slot 1 of CTA j - 1, slot 0 of CTAs j .. j + n - 2
     while (j + n - 1 < c.ctas && stretch(c.total, c.ctas, j + n - 1) < c.te)
         ++n;
     const float *first = partial<NT>(L, j - 1, 1), *rest = partial<NT>(L, j, 0);
     auto piece = [&](int i) { return i == 0 ? first : rest + static_cast<size_t>(i - 1) * 2 * partial_floats<NT>(); };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32)
-        top = fmaxf(top, piece(i)[NT * kHeadDim + r]);
+    float top[kR], sum[kR];
+    float4 acc[kR];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < kR; ++e) {
+        top[e] = -INFINITY;
+        for (int i = lane; i < n; i += 32)
+            top[e] = fmaxf(top[e], piece(i)[NT * kHeadDim + r0 + e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kR; ++e) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], d));
+        sum[e] = 0.f;
+        acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < n) {
-            const float *p = piece(i0 + lane);
-            w = attn::ex2(p[NT * kHeadDim + r] - top);
-            sum += w * p[NT * (kHeadDim + 1) + r];
+        float w[kR];
+#pragma unroll
+        for (int e = 0; e < kR; ++e) {
+            w[e] = 0.f;
+            if (i0 + lane < n) {
+                const float *p = piece(i0 + lane);
+                w[e] = attn::ex2(p[NT * kHeadDim + r0 + e] - top[e]);
+                sum[e] += w[e] * p[NT * (kHeadDim + 1) + r0 + e];
+            }
         }
         const int m = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll(kR == 1 ? 4 : 1)
         for (int i = 0; i < m; ++i) {
-            const float wi = __shfl_sync(kFull, w, i);
-            const float4 o = reinterpret_cast<const float4 *>(piece(i0 + i) + r * kHeadDim)[lane];
-            acc.x = fmaf(wi, o.x, acc.x);
-            acc.y = fmaf(wi, o.y, acc.y);
-            acc.z = fmaf(wi, o.z, acc.z);
-            acc.w = fmaf(wi, o.w, acc.w);
+            const float4 *o = reinterpret_cast<const float4 *>(piece(i0 + i) + r0 * kHeadDim) + lane;
+#pragma unroll
+            for (int e = 0; e < kR; ++e) {
+                const float wi = __shfl_sync(kFull, w[e], i);
+                const float4 v = o[e * (kHeadDim / 4)];
+                acc[e].x = fmaf(wi, v.x, acc[e].x);
+                acc[e].y = fmaf(wi, v.y, acc[e].y);
+                acc[e].z = fmaf(wi, v.z, acc[e].z);
+                acc[e].w = fmaf(wi, v.w, acc[e].w);
+            }
         }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        sum += __shfl_xor_sync(kFull, sum, d);
-    const float inv = L.v_scale / sum;
-    const int flat = c.row + r, tok = flat / L.G;
-    const int64_t at = (static_cast<int64_t>(c.tok0) + tok) * L.Hq + c.h * L.G + flat - tok * L.G;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2 *>(L.O + at * kHeadDim)[lane] =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    if (L.lse != nullptr && lane == 0)
-        L.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
+    for (int e = 0; e < kR; ++e) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            sum[e] += __shfl_xor_sync(kFull, sum[e], d);
+        if (r0 + e >= c.rows)
+            break;
+        const float inv = L.v_scale / sum[e];
+        const int flat = c.row + r0 + e, tok = token_of(L, flat);
+        const int64_t at = (static_cast<int64_t>(c.tok0) + tok) * L.Hq + c.h * L.G + flat - tok * L.G;
+        const __nv_bfloat162 a = __floats2bfloat162_rn(acc[e].x * inv, acc[e].y * inv), b = __floats2bfloat162_rn(acc[e].z * inv, acc[e].w * inv);
+        reinterpret_cast<uint2 *>(L.O + at * kHeadDim)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        if (L.lse != nullptr && lane == 0)
+            L.lse[at] = (top[e] + log2f(sum[e])) * 0.6931471805599453f;
+    }
 }
 
 // Lets k_chunk_merge come up; every thread of the attention kernels calls it.
@@ -535,7 +588,7 @@ cudaError_t merge_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, (NT + 3) / 4);
+    cfg.gridDim = dim3(ctas, NT <= 64 ? NT / 4 : 16);
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cfg.attrs = &early;

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 v[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = r0 + 4 * i, flat = j.row + r, tok = flat / L.G, head = j.h * L.G + flat - tok * L.G;
+                    const int r = r0 + 4 * i, flat = j.row + r, tok = token_of(L, flat), head = j.h * L.G + flat - tok * L.G;
                     const bool real = r < j.rows;
                     v[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (real)

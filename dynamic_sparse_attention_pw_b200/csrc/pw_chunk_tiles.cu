@@ -90,6 +90,14 @@ __device__ __forceinline__ void e4m3x16_to_f16(const uint4 x, uint4 &h0, uint4 &
     h1 = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
+// 32 bytes, a whole sector: rows of one thread each, so a warp's stores touch 32 places.
+__device__ __forceinline__ void store32(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+                 "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float max32(const uint32_t (&x)[32])
 {
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             const int last_pos = L.pm.max_pages * kPageTokens - 1;
-            auto pos_of = [&](int row) { return static_cast<int>(min(static_cast<int64_t>(j.ctx) + (j.row + row) / L.G, static_cast<int64_t>(last_pos))); };
+            auto pos_of = [&](int row) { return static_cast<int>(min(static_cast<int64_t>(j.ctx) + token_of(L, j.row + row), static_cast<int64_t>(last_pos))); };
             const bool real = r < j.rows;
             const int pos = real ? pos_of(r) : -1;
             const int pos_lo = pos_of(128 * a), pos_hi = pos_of(min(j.rows, 128 * a + 128) - 1);
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // ---- the end of the tile ----
             float *const part = j.slot >= 0 ? partial<kRows>(L, cta, j.slot) : nullptr;
-            const int flat = j.row + r, tok = flat / L.G;
+            const int flat = j.row + r, tok = token_of(L, flat);
             const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
             float l0, l1;
             unpack2(add2(l[0], l[1]), l0, l1);
@@ -287,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_addr + 32 * ch, o);
                 tmem_ld_wait(o);
                 if (real && part != nullptr) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(part + r * kHeadDim + 32 * ch);
+                    float *dst = part + r * kHeadDim + 32 * ch;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int e = 0; e < 32; e += 8)
+                        store32(dst + e, o + e);
                 } else if (real) {
                     uint32_t w[16];
 #pragma unroll
@@ -298,10 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
                         w[e] = *reinterpret_cast<const uint32_t *>(&b);
                     }
-                    uint4 *dst = reinterpret_cast<uint4 *>(L.O + at * kHeadDim + 32 * ch);
+                    uint16_t *dst = L.O + at * kHeadDim + 32 * ch;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    for (int e = 0; e < 16; e += 4)
+                        reinterpret_cast<uint4 *>(dst)[e / 4] = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                 }
             }
             tc_fence_before();
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 12) {
         // ---------------- queries; V to f16 ----------------
-        const int w = warp - 8, hl = lane >> 4, l16 = lane & 15, t = tid - 256;
+        const int t = tid - 256;
         uint32_t nt[2] = {0, 0}, c = 0;
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
@@ -332,26 +340,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_wait(&sm.q_empty[a], (nt[a] & 1u) ^ 1u, ab);
                 if (!ok)
                     break;
-                // sixteen lanes a row, four rows of a half-warp at a time
-#pragma unroll 1
-                for (int r0 = 2 * w + hl; r0 < kHalf; r0 += 32) {
-                    uint4 v[4];
+                // a thread a row
+                const int r = 128 * a + t, flat = j.row + r, tok = token_of(L, flat);
+                const bool real = r < j.rows;
+                const uint4 *src = reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
+                                                                   static_cast<int64_t>(j.h * L.G + flat - tok * L.G) * L.q_sh);
+                uint4 v[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 128 * a + r0 + 8 * i, flat = j.row + r, tok = flat / L.G, head = j.h * L.G + flat - tok * L.G;
-                        v[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < j.rows)
-                            v[i] = __ldg(reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
-                                                                         static_cast<int64_t>(head) * L.q_sh) + l16);
-                    }
+                for (int i = 0; i < 16; ++i)
+                    v[i] = real ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t e = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + 8 * i;
-                        const float f = stage_q_row(v[i], sm.q[a][0], r, kHalf + r, l16, L.score_scale);
-                        if (l16 == 0)
-                            sm.c[a][nt[a] & 1u][r] = f;
-                    }
+                for (int i = 0; i < 16; ++i)
+                    e = __vmaxu2(__vmaxu2(__vmaxu2(e, v[i].x & 0x7F807F80u), __vmaxu2(v[i].y & 0x7F807F80u, v[i].z & 0x7F807F80u)), v[i].w & 0x7F807F80u);
+                e = max(e >> 23, (e >> 7) & 0xFFu);
+                const int sh = q_exp(e);
+                const float up = exp2i(sh);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint2 a1, a2, b1, b2;
+                    split_q8(v[2 * i], up, a1, a2);
+                    split_q8(v[2 * i + 1], up, b1, b2);
+                    const uint32_t at = attn::swz(t, i);
+                    *reinterpret_cast<uint4 *>(sm.q[a][0] + at) = make_uint4(a1.x, a1.y, b1.x, b1.y);
+                    *reinterpret_cast<uint4 *>(sm.q[a][1] + at) = make_uint4(a2.x, a2.y, b2.x, b2.y);
                 }
+                sm.c[a][nt[a] & 1u][t] = q_factor(e, L.score_scale);
                 fence_proxy_async_smem();
                 warp_arrive(&sm.q_full[a], lane);
                 ++nt[a];

@@ -205,6 +205,9 @@ pw_status pw_chunk_attn(const void *Q, int64_t q_stride_t, int64_t q_stride_h, i
     L.Hq = Hq;
     L.Hkv = Hkv;
     L.G = Hq / Hkv;
+    while ((1ll << L.g_shift) < L.G)
+        ++L.g_shift;
+    L.g_mul = static_cast<uint32_t>((((1ull << L.g_shift) - L.G) << 32) / L.G + 1);
     L.window = window;
     L.max_q_len = max_q_len;
     L.score_scale = static_cast<float>(scale);
