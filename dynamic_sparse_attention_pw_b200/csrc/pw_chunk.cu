@@ -65,8 +65,9 @@ size_t chunk_workspace(int, int64_t, int Hq, int Hkv, int max_q_len)
     return rows <= kFewRows ? chunk::decode_workspace(static_cast<int>(rows)) : chunk::tiles_workspace();
 }
 
-cudaError_t chunk_launch(const ChunkLaunch &L, cudaStream_t st)
+cudaError_t chunk_launch(const ChunkLaunch &launch, cudaStream_t st)
 {
+    ChunkLaunch L = launch;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
@@ -74,6 +75,7 @@ cudaError_t chunk_launch(const ChunkLaunch &L, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     const int ctas = std::min(sms, chunk::kMaxCtas);
+    L.ctas_mul = ~0ull / ctas + 1; // of no use, and not used, for one CTA
     const int64_t rows = rows_of(L.Hq, L.Hkv, L.max_q_len);
     return rows <= kFewRows ? chunk::decode_launch(L, static_cast<int>(rows), ctas, st) : chunk::tiles_launch(L, ctas, st);
 }

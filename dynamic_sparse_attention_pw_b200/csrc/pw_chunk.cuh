@@ -6,7 +6,7 @@
 // its rows see) are cut into blocks of 128 positions, two pages.  All blocks of all tiles form one
 // line, ordered by (sequence, kv head, tile, block), and the CTAs take equal stretches of it, so
 // one long context, many short ones and any mixture fill the GPU alike.  The lengths are read
-// on the device, by every CTA for itself (a block scan over the sequences).
+// on the device, by the load warp of every CTA for itself.
 //
 // A tile that lies within one stretch is finished by its CTA.  One that is cut leaves partial
 // results (fp32 accumulator, running maximum, sum) in the workspace, at most two of a CTA: the end
@@ -58,11 +58,30 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b)
     return d;
 }
 
+// What the tiles of a call depend on besides their sequence.
+struct Shape {
+    int G, window, last; // last position a page table's row can hold
+    uint32_t mul, shift; // n / G = (n * mul / 2^32 + n) >> shift
+
+    __device__ __forceinline__ explicit Shape(const ChunkLaunch &L)
+        : G(L.G), window(L.window), last(L.pm.max_pages * kPageTokens - 1), mul(L.g_mul), shift(L.g_shift)
+    {
+    }
+    __device__ __forceinline__ int token(int row) const // of a flat row
+    {
+        const uint32_t n = static_cast<uint32_t>(row);
+        return static_cast<int>((__umulhi(n, mul) + n) >> shift);
+    }
+    __device__ __forceinline__ int position(int ctx, int token) const
+    {
+        return static_cast<int>(min(static_cast<uint32_t>(ctx) + static_cast<uint32_t>(token), static_cast<uint32_t>(last)));
+    }
+};
+
 struct Sequence {
-    int row0;     // first row of Q (token) of the sequence
-    int qlen;     // new tokens
-    int64_t ctx;  // tokens before them
-    int64_t last; // last position the page table's row can hold
+    int row0; // first row of Q (token) of the sequence
+    int qlen; // new tokens
+    int ctx;  // tokens before them
 };
 
 // Contents that the arguments rule out (offsets outside [0, T] or falling, a negative context, a
@@ -70,24 +89,17 @@ struct Sequence {
 // the caller's buffers.
 __device__ __forceinline__ Sequence sequence(const ChunkLaunch &L, int b)
 {
-    Sequence s;
     const int T = static_cast<int>(L.tb.T);
     const int c0 = __ldg(L.tb.cu + b), c1 = __ldg(L.tb.cu + b + 1);
     const int ctx = L.tb.ctx != nullptr ? __ldg(L.tb.ctx + b) : 0;
+    Sequence s;
     s.row0 = min(max(c0, 0), T);
     s.qlen = max(min(max(c1, 0), T) - s.row0, 0);
     s.ctx = max(ctx, 0);
-    s.last = static_cast<int64_t>(L.pm.max_pages) * kPageTokens - 1;
-    if (c0 != s.row0 || c1 != s.row0 + s.qlen || (s.qlen > 0 && (ctx < 0 || s.ctx + s.qlen - 1 > s.last)))
+    const int64_t end = static_cast<int64_t>(s.ctx) + s.qlen, room = static_cast<int64_t>(L.pm.max_pages) * kPageTokens;
+    if (c0 != s.row0 || c1 != s.row0 + s.qlen || (s.qlen > 0 && (ctx < 0 || end > room)))
         set_status(L.status, PW_ERR_INVALID_ARG);
     return s;
-}
-
-// Token of a flat row: row / G.
-__device__ __forceinline__ int token_of(const ChunkLaunch &L, int row)
-{
-    const uint32_t n = static_cast<uint32_t>(row);
-    return static_cast<int>((__umulhi(n, L.g_mul) + n) >> L.g_shift);
 }
 
 struct Tile {
@@ -96,50 +108,46 @@ struct Tile {
     int blk0, nblk; // their blocks
 };
 
-__device__ __forceinline__ int position(const Sequence &s, int token)
-{
-    return static_cast<int>(min(s.ctx + token, s.last));
-}
-
 template <int NT>
-__device__ __forceinline__ Tile tile_of(const ChunkLaunch &L, const Sequence &s, int i)
+__device__ __forceinline__ Tile tile_of(const Shape &p, int qlen, int ctx, int i)
 {
     Tile t;
     t.row = i * NT;
-    t.rows = min(s.qlen * L.G - t.row, NT);
-    t.hi = position(s, token_of(L, t.row + t.rows - 1)) + 1;
-    t.lo = L.window > 0 ? max(position(s, token_of(L, t.row)) - L.window + 1, 0) : 0;
+    t.rows = min(qlen * p.G - t.row, NT);
+    t.hi = p.position(ctx, p.token(t.row + t.rows - 1)) + 1;
+    t.lo = p.window > 0 ? max(p.position(ctx, p.token(t.row)) - p.window + 1, 0) : 0;
     t.blk0 = t.lo / kBlock;
     t.nblk = (t.hi + kBlock - 1) / kBlock - t.blk0;
     return t;
 }
 
 template <int NT>
-__device__ __forceinline__ int tiles_of(const ChunkLaunch &L, const Sequence &s)
+__device__ __forceinline__ int tiles_of(const Shape &p, int qlen)
 {
-    return (s.qlen * L.G + NT - 1) / NT;
+    return (qlen * p.G + NT - 1) / NT;
 }
 
-// Blocks of one kv head of the sequences b of a warp's lanes (b >= B: 0).  A lane counts a few tiles by
-// itself, the warp those of a sequence of many together.
+// Blocks of one kv head of each lane's sequence.  A lane counts a few tiles by itself, the warp those
+// of a sequence of many together.  Not inlined: it runs once or twice, from a cold instruction cache.
 template <int NT>
-__device__ __forceinline__ int64_t head_blocks(const ChunkLaunch &L, int b)
+__device__ __noinline__ int64_t head_blocks(const Shape p, int qlen, int ctx, int lane)
 {
-    constexpr int kAlone = 4;
-    const int lane = threadIdx.x & 31;
-    const Sequence s = b < L.tb.B ? sequence(L, b) : Sequence{0, 0, 0, 0};
-    const int tiles = tiles_of<NT>(L, s);
+    constexpr int kAlone = 2;
+    const int tiles = tiles_of<NT>(p, qlen);
     int64_t n = 0;
-    if (tiles <= kAlone)
-        for (int i = 0; i < tiles; ++i)
-            n += tile_of<NT>(L, s, i).nblk;
-    for (uint32_t many = __ballot_sync(kFull, tiles > kAlone); many != 0u; many &= many - 1) {
-        const int from = __ffs(many) - 1;
-        const Sequence o{__shfl_sync(kFull, s.row0, from), __shfl_sync(kFull, s.qlen, from), __shfl_sync(kFull, s.ctx, from),
-                         __shfl_sync(kFull, s.last, from)};
+    for (uint32_t many = __ballot_sync(kFull, tiles > kAlone), first = 1; first != 0u || many != 0u; first = 0) {
+        // the first round: every lane its own few tiles; the others: a sequence of many
+        const int from = first != 0u ? lane : __ffs(many) - 1;
+        const int q = __shfl_sync(kFull, qlen, from), c = __shfl_sync(kFull, ctx, from), e = __shfl_sync(kFull, tiles, from);
+        const bool alone = first != 0u;
         int64_t m = 0;
-        for (int i = lane, e = __shfl_sync(kFull, tiles, from); i < e; i += 32)
-            m += tile_of<NT>(L, o, i).nblk;
+        for (int i = alone ? 0 : lane, end = alone && e > kAlone ? 0 : e; i < end; i += alone ? 1 : 32)
+            m += tile_of<NT>(p, q, c, i).nblk;
+        if (alone) {
+            n = m;
+            continue;
+        }
+        many &= many - 1;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             m += __shfl_xor_sync(kFull, m, d);
@@ -149,91 +157,13 @@ __device__ __forceinline__ int64_t head_blocks(const ChunkLaunch &L, int b)
     return n;
 }
 
-struct Plan {
-    int64_t total;   // blocks of the whole call
-    int64_t x0, x1;  // this CTA's stretch
-    int64_t b_start; // first block of sequence b0
-    int64_t per_head; // blocks of one kv head of sequence b0
-    int b0;          // sequence that x0 lies in
-    int ctas;        // CTAs with work
-    int64_t scan[33];
+// The line of all blocks in equal stretches, the first `longer` of them one block longer.
+struct Stretches {
+    int64_t len;
+    int longer, ctas;
+
+    __device__ __forceinline__ int64_t begin(int j) const { return len * j + min(j, longer); }
 };
-
-// First block of stretch j: equal stretches, the first ones one longer.
-__device__ __forceinline__ int64_t stretch(int64_t total, int ctas, int j)
-{
-    const int64_t q = total / ctas;
-    return q * j + min(static_cast<int64_t>(j), total - q * ctas);
-}
-
-// Block-wide inclusive scan of v; returns it and the sum in `sum`.  scratch: 33 words.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *scratch, int64_t &sum)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(kFull, v, d);
-        if (lane >= d)
-            v += o;
-    }
-    __syncthreads();
-    if (lane == 31)
-        scratch[warp] = v;
-    __syncthreads();
-    int64_t before = 0;
-    sum = 0;
-    for (int i = 0; i < nw; ++i) {
-        if (i < warp)
-            before += scratch[i];
-        sum += scratch[i];
-    }
-    return v + before;
-}
-
-// Every thread of the CTA calls it; the plan is in shared memory afterwards.  min_blocks: a CTA is
-// given at least that many blocks.
-template <int NT>
-__device__ void make_plan(const ChunkLaunch &L, Plan &p, int cta, int min_blocks)
-{
-    const int nt = blockDim.x, tid = threadIdx.x, B = L.tb.B;
-    int64_t mine = head_blocks<NT>(L, tid), total = 0;
-    int64_t all = mine;
-    for (int b = nt; b < B; b += nt)
-        all += head_blocks<NT>(L, b + tid);
-    (void)block_scan(all, p.scan, total);
-    total *= L.Hkv;
-    const int ctas = static_cast<int>(max(min(static_cast<int64_t>(gridDim.x), total / min_blocks), static_cast<int64_t>(1)));
-    const int64_t x0 = cta < ctas ? stretch(total, ctas, cta) : total;
-    const int64_t x1 = cta < ctas ? stretch(total, ctas, cta + 1) : total;
-    if (tid == 0) {
-        p.total = total;
-        p.x0 = x0;
-        p.x1 = x1;
-        p.ctas = ctas;
-        p.b0 = 0;
-        p.b_start = 0;
-        p.per_head = 1;
-    }
-    int64_t run = 0;
-    if (x0 < x1) { // uniform
-        for (int base = 0; base < B; base += nt) {
-            const int b = base + tid;
-            if (base > 0)
-                mine = head_blocks<NT>(L, b);
-            int64_t sum;
-            const int64_t incl = run + block_scan(mine, p.scan, sum) * L.Hkv;
-            if (mine > 0 && incl - mine * L.Hkv <= x0 && x0 < incl) {
-                p.b0 = b;
-                p.b_start = incl - mine * L.Hkv;
-                p.per_head = mine;
-            }
-            run += sum * L.Hkv;
-            if (run > x0)
-                break;
-        }
-    }
-    __syncthreads();
-}
 
 // One piece of a tile, as the roles of a CTA hand it on.
 struct Job {
@@ -249,8 +179,9 @@ struct Job {
 
 // Where the tile that stretch j starts in was cut, for k_chunk_merge.
 struct Cut {
-    int64_t total, ts, te; // all blocks; first block of the tile and the one behind its last
-    int ctas, inside;      // inside: the stretch starts behind the tile's first block
+    Stretches all;
+    int64_t ts, te; // first block of the tile and the one behind its last
+    int inside;     // the stretch starts behind the tile's first block
     int row, rows, h, tok0;
 };
 
@@ -273,29 +204,88 @@ __device__ __forceinline__ float *partial(const ChunkLaunch &L, int j, int s)
 // The pieces of a CTA's stretch, one after the other; a warp runs it (uniformly).
 template <int NT>
 struct Pieces {
+    Stretches all;
     int64_t x, x1;
     int b, h, i, off; // next piece: tile i of (b, h), from its block off on
     Sequence s;
     int tiles;
+    bool first;
 
-    __device__ __forceinline__ void begin(const ChunkLaunch &L, const Plan &p, Cut *cuts, int cta, int lane)
+    __device__ __forceinline__ void begin(const ChunkLaunch &L, const Shape &p, int cta, int lane)
     {
-        x = p.x0;
-        x1 = p.x1;
+        const int B = L.tb.B, grid = gridDim.x;
+        // All blocks.  Four sequences a lane at once, so that their loads overlap; the first 128 counts stay.
+        int64_t mine[4] = {0, 0, 0, 0}, total = 0;
+        for (int base = 0; base < B; base += 128) {
+            Sequence q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[e] = base + 32 * e + lane < B ? sequence(L, base + 32 * e + lane) : Sequence{0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (base + 32 * e < B) {
+                    const int64_t n = head_blocks<NT>(p, q[e].qlen, q[e].ctx, lane);
+                    total += n;
+                    if (base == 0)
+                        mine[e] = n;
+                }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            total += __shfl_xor_sync(kFull, total, d);
+        total *= L.Hkv;
+        all.ctas = static_cast<int>(min(static_cast<int64_t>(grid), max(total, static_cast<int64_t>(1))));
+        all.len = grid == 1 ? total : total < grid ? min(total, static_cast<int64_t>(1)) : static_cast<int64_t>(__umul64hi(total, L.ctas_mul));
+        all.longer = total < grid ? 0 : static_cast<int>(total - all.len * grid);
+        x = cta < all.ctas ? all.begin(cta) : total;
+        x1 = cta < all.ctas ? all.begin(cta + 1) : total;
+        first = true;
         if (x >= x1) {
-            if (lane == 0 && cta < kMaxCtas)
-                cuts[cta].inside = 0;
+            none(L, cta, lane);
             return;
         }
-        b = p.b0;
+        // the sequence and head that x lies in
+        int64_t rest = x, per_head = 1;
+        b = -1;
+        for (int base = 0; b < 0 && base < B; base += 32) {
+            int64_t n = base == 0 ? mine[0] : base == 32 ? mine[1] : base == 64 ? mine[2] : mine[3];
+            if (base >= 128) {
+                const Sequence q = base + lane < B ? sequence(L, base + lane) : Sequence{0, 0, 0};
+                n = head_blocks<NT>(p, q.qlen, q.ctx, lane);
+            }
+            int64_t incl = n * L.Hkv;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(kFull, incl, d);
+                if (lane >= d)
+                    incl += o;
+            }
+            const uint32_t beyond = __ballot_sync(kFull, incl > rest);
+            if (beyond != 0u) {
+                const int k = __ffs(beyond) - 1;
+                b = base + k;
+                per_head = __shfl_sync(kFull, n, k);
+                rest -= __shfl_sync(kFull, incl - n * L.Hkv, k);
+            } else {
+                rest -= __shfl_sync(kFull, incl, 31);
+            }
+        }
+        if (b < 0) { // cannot happen while the lengths stay as they were
+            none(L, cta, lane);
+            return;
+        }
+        for (h = 0;; h += 32) { // heads that end at or before x
+            const int k = __popc(__ballot_sync(kFull, (h + lane + 1) * per_head <= rest));
+            if (k < 32) {
+                h += k;
+                break;
+            }
+        }
+        rest -= h * per_head;
         s = sequence(L, b);
-        tiles = tiles_of<NT>(L, s);
-        int64_t rest = x - p.b_start;
-        h = static_cast<int>(rest / p.per_head);
-        rest -= h * p.per_head;
-        // 32 tiles at a time
-        for (i = 0;; i += 32) {
-            int n = i + lane < tiles ? tile_of<NT>(L, s, i + lane).nblk : 0;
+        tiles = tiles_of<NT>(p, s.qlen);
+        for (i = 0;; i += 32) { // 32 tiles at a time
+            const int n = i + lane < tiles ? tile_of<NT>(p, s.qlen, s.ctx, i + lane).nblk : 0;
             int incl = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -308,30 +298,33 @@ struct Pieces {
                 const int k = __ffs(beyond) - 1;
                 i += k;
                 off = static_cast<int>(rest) - __shfl_sync(kFull, incl - n, k);
-                break;
-            }
-            const int sum = __shfl_sync(kFull, incl, 31);
-            if (sum == 0 && i + 32 >= tiles) { // cannot happen while the lengths stay as they were
-                x = x1;
-                if (lane == 0)
-                    cuts[cta].inside = 0;
                 return;
             }
-            rest -= sum;
-        }
-        if (lane == 0) {
-            const Tile t = tile_of<NT>(L, s, i);
-            cuts[cta] = Cut{p.total, x - off, x - off + t.nblk, p.ctas, off > 0, t.row, t.rows, h, s.row0};
+            if (i + 32 >= tiles) { // as above
+                none(L, cta, lane);
+                return;
+            }
+            rest -= __shfl_sync(kFull, incl, 31);
         }
     }
 
-    __device__ __forceinline__ bool next(const ChunkLaunch &L, Job &j)
+    __device__ __forceinline__ void none(const ChunkLaunch &L, int cta, int lane)
+    {
+        x = x1;
+        if (lane == 0)
+            static_cast<Cut *>(L.workspace)[cta].inside = 0;
+    }
+
+    __device__ __forceinline__ bool next(const ChunkLaunch &L, const Shape &p, int cta, int lane, Job &j)
     {
         if (x >= x1)
             return false;
-        const Tile t = tile_of<NT>(L, s, i);
+        const Tile t = tile_of<NT>(p, s.qlen, s.ctx, i);
         const int n = static_cast<int>(min(static_cast<int64_t>(t.nblk - off), x1 - x));
-        j = Job{n, t.blk0 + off, t.lo, t.hi, t.row, t.rows, b, h, s.row0, static_cast<int>(s.ctx), off > 0 ? 0 : (n < t.nblk ? 1 : -1)};
+        j = Job{n, t.blk0 + off, t.lo, t.hi, t.row, t.rows, b, h, s.row0, s.ctx, off > 0 ? 0 : (n < t.nblk ? 1 : -1)};
+        if (first && lane == 0)
+            static_cast<Cut *>(L.workspace)[cta] = Cut{all, x - off, x - off + t.nblk, off > 0, t.row, t.rows, h, s.row0};
+        first = false;
         x += n;
         off = 0;
         if (++i == tiles) {
@@ -340,7 +333,7 @@ struct Pieces {
                 h = 0;
                 while (x < x1 && ++b < L.tb.B) {
                     s = sequence(L, b);
-                    tiles = tiles_of<NT>(L, s);
+                    tiles = tiles_of<NT>(p, s.qlen);
                     if (tiles > 0)
                         break;
                 }
@@ -511,10 +504,10 @@ __global__ void __launch_bounds__(128, NT <= 32 ? 16 : 8) k_chunk_merge(const Ch
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int j = blockIdx.x, lane = threadIdx.x & 31, r0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * kR;
     const Cut c = reinterpret_cast<const Cut *>(L.workspace)[j];
-    if (!c.inside || r0 >= c.rows || stretch(c.total, c.ctas, j - 1) > c.ts)
+    if (!c.inside || r0 >= c.rows || c.all.begin(j - 1) > c.ts)
         return;
     int n = 1; // pieces: slot 1 of CTA j - 1, slot 0 of CTAs j .. j + n - 2
-    while (j + n - 1 < c.ctas && stretch(c.total, c.ctas, j + n - 1) < c.te)
+    while (j + n - 1 < c.all.ctas && c.all.begin(j + n - 1) < c.te)
         ++n;
     const float *first = partial<NT>(L, j - 1, 1), *rest = partial<NT>(L, j, 0);
     auto piece = [&](int i) { return i == 0 ? first : rest + static_cast<size_t>(i - 1) * 2 * partial_floats<NT>(); };
@@ -568,7 +561,7 @@ __global__ void __launch_bounds__(128, NT <= 32 ? 16 : 8) k_chunk_merge(const Ch
         if (r0 + e >= c.rows)
             break;
         const float inv = L.v_scale / sum[e];
-        const int flat = c.row + r0 + e, tok = token_of(L, flat);
+        const int flat = c.row + r0 + e, tok = Shape(L).token(flat);
         const int64_t at = (static_cast<int64_t>(c.tok0) + tok) * L.Hq + c.h * L.G + flat - tok * L.G;
         const __nv_bfloat162 a = __floats2bfloat162_rn(acc[e].x * inv, acc[e].y * inv), b = __floats2bfloat162_rn(acc[e].z * inv, acc[e].w * inv);
         reinterpret_cast<uint2 *>(L.O + at * kHeadDim)[lane] =

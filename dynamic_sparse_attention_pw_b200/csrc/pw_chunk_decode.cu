@@ -47,7 +47,6 @@ constexpr int kJobs = 4;
 // Query tiles: S runs up to two blocks, so up to two tiles, ahead of the products, and a tile's slot is
 // free when its results are written.
 constexpr int kQ = 3;
-constexpr int kMinBlocks = 1;
 constexpr uint32_t kBarAll = 5; // named barrier of all softmax warps (the groups' halves: 1 to 4)
 constexpr float kAbove = 4.f;  // a row's reference moves to this much above its largest score (base 2)
 
@@ -69,7 +68,6 @@ struct __align__(1024) DecSmem {
     float alpha[2][NT];               // [group]: factor when it moves
     float red[2][4][NT];              // [group][key quarter]: block maxima, row sums
     Job job[kJobs];
-    Plan plan;
     uint64_t job_full[kJobs], job_empty[kJobs];
     uint64_t q_full[kQ], q_empty[kQ];
     uint64_t k_full[kStages], v_full[kStages], st_empty[kStages];
@@ -175,17 +173,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&sm.tmem, kTmemCols);
         tmem_relinquish();
     }
-    make_plan<NT>(L, sm.plan, cta, kMinBlocks);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     int32_t *const ab = &sm.abort_flag;
+    const Shape shape(L);
 
     if (warp == 0) {
         // ---------------- load ----------------
         Pieces<NT> pieces;
-        pieces.begin(L, sm.plan, reinterpret_cast<Cut *>(L.workspace), cta, lane);
+        pieces.begin(L, shape, cta, lane);
         // slots of the 32 pages of job j from block k on, one a lane
         auto fetch = [&](const Job &j, int k) {
             const int pg = 2 * (j.blk0 + k) + lane; // between the pages that hold a key of the tile
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint32_t c = 0;
         Job j;
-        bool more = pieces.next(L, j), ok = true;
+        bool more = pieces.next(L, shape, cta, lane, j), ok = true;
         int ids = more ? fetch(j, 0) : -1;
         for (uint32_t n = 0; ok; ++n) {
             ok = warp_wait(&sm.job_empty[n % kJobs], ((n / kJobs) & 1u) ^ 1u, ab);
@@ -239,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (k == ahead) {
-                    more = pieces.next(L, jn);
+                    more = pieces.next(L, shape, cta, lane, jn);
                     if (more)
                         ids_n = fetch(jn, 0);
                 }
@@ -323,20 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t qb = n % kQ;
             if (!warp_wait(&sm.q_empty[qb], ((n / kQ) & 1u) ^ 1u, ab))
                 break;
-            const Sequence s = sequence(L, j.b);
             // sixteen lanes a row, two rows of a half-warp at a time
             for (int r0 = 2 * (warp - 2) + half; r0 < NT; r0 += 8) {
                 uint4 v[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = r0 + 4 * i, flat = j.row + r, tok = token_of(L, flat), head = j.h * L.G + flat - tok * L.G;
+                    const int r = r0 + 4 * i, flat = j.row + r, tok = shape.token(flat), head = j.h * L.G + flat - tok * L.G;
                     const bool real = r < j.rows;
                     v[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (real)
                         v[i] = __ldg(reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
                                                                      static_cast<int64_t>(head) * L.q_sh) + l);
                     if (l == 0) {
-                        sm.pos[qb][r] = real ? position(s, tok) : -1;
+                        sm.pos[qb][r] = real ? shape.position(j.ctx, tok) : -1;
                         sm.at[qb][r] = (j.tok0 + tok) * L.Hq + head;
                     }
                 }

@@ -33,7 +33,6 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;
 constexpr int kHalf = 128;
 constexpr int kJobs = 4;
-constexpr int kMinBlocks = 1;
 constexpr int kNK = 3, kNV = 2; // K and V stages
 constexpr float kRaise = 15.f;  // a row's reference moves when a score exceeds it by more (base 2); f16 ends at 2^16
 
@@ -44,7 +43,6 @@ struct __align__(1024) TileSmem {
     uint8_t v16[2][2][kBlock * 128]; // [block % 2][dims 0-63, 64-127][key][dim] f16, swizzled
     float c[2][2][kHalf];           // [half][its tile % 2]: factor of a row's scores
     Job job[kJobs];
-    Plan plan;
     uint64_t job_full[kJobs], job_empty[kJobs];
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kNK], k_empty[kNK], v_full[kNV], v_empty[kNV];
@@ -174,12 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
-    make_plan<kRows>(L, sm.plan, cta, kMinBlocks);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     int32_t *const ab = &sm.abort_flag;
+    const Shape shape(L);
 
     if (warp < 8) {
         // ---------------- softmax ----------------
@@ -199,8 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_arrive(&sm.job_empty[n % kJobs], lane);
                 continue;
             }
-            const int last_pos = L.pm.max_pages * kPageTokens - 1;
-            auto pos_of = [&](int row) { return static_cast<int>(min(static_cast<int64_t>(j.ctx) + token_of(L, j.row + row), static_cast<int64_t>(last_pos))); };
+            auto pos_of = [&](int row) { return shape.position(j.ctx, shape.token(j.row + row)); };
             const bool real = r < j.rows;
             const int pos = real ? pos_of(r) : -1;
             const int pos_lo = pos_of(128 * a), pos_hi = pos_of(min(j.rows, 128 * a + 128) - 1);
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // ---- the end of the tile ----
             float *const part = j.slot >= 0 ? partial<kRows>(L, cta, j.slot) : nullptr;
-            const int flat = j.row + r, tok = token_of(L, flat);
+            const int flat = j.row + r, tok = shape.token(flat);
             const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
             float l0, l1;
             unpack2(add2(l[0], l[1]), l0, l1);
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok)
                     break;
                 // a thread a row
-                const int r = 128 * a + t, flat = j.row + r, tok = token_of(L, flat);
+                const int r = 128 * a + t, flat = j.row + r, tok = shape.token(flat);
                 const bool real = r < j.rows;
                 const uint4 *src = reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
                                                                    static_cast<int64_t>(j.h * L.G + flat - tok * L.G) * L.q_sh);
@@ -406,14 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 12) {
             // ---------------- load ----------------
             Pieces<kRows> pieces;
-            pieces.begin(L, sm.plan, reinterpret_cast<Cut *>(L.workspace), cta, lane);
+            pieces.begin(L, shape, cta, lane);
             auto fetch = [&](const Job &j, int k) { // slots of the 32 pages of job j from block k on, one a lane
                 const int pg = 2 * (j.blk0 + k) + lane; // between the pages that hold a key of the tile
                 return pg >= (j.lo >> 6) && pg <= ((j.hi - 1) >> 6) && pg < 2 * (j.blk0 + j.nblk) ? phys_slot(L, j.b, pg) : -1;
             };
             uint32_t c = 0;
             Job j;
-            bool more = pieces.next(L, j), ok = true;
+            bool more = pieces.next(L, shape, cta, lane, j), ok = true;
             int ids = more ? fetch(j, 0) : -1;
             for (uint32_t n = 0; ok; ++n) {
                 ok = warp_wait(&sm.job_empty[n % kJobs], ((n / kJobs) & 1u) ^ 1u, ab);
@@ -466,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     if (k == ahead) {
-                        more = pieces.next(L, jn);
+                        more = pieces.next(L, shape, cta, lane, jn);
                         if (more)
                             ids_n = fetch(jn, 0);
                     }

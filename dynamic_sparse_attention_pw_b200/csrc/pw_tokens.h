@@ -68,6 +68,7 @@ struct ChunkLaunch {
     TokenBatch tb;
     int Hq, Hkv, G, window, max_q_len;
     uint32_t g_mul, g_shift; // n / G = (n * g_mul / 2^32 + n) >> g_shift for 0 <= n < 2^31
+    uint64_t ctas_mul; // n / CTAs = n * ctas_mul / 2^64 (n below 2^56)
     float score_scale; // sm_scale * k_scale * log2 e: scores to base-2 exponents
     float v_scale;
     uint16_t *O; // bf16 bits
