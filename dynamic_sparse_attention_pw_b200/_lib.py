@@ -1,6 +1,7 @@
-"""ctypes loader of libpw.so (the C ABI declared in include/pw.h).
+"""ctypes loader of libpw.so (the C ABI declared in include/pw.h), and of the compiled marshalling of the
+calls on new tokens (csrc/pw_binding.cpp).
 
-No fallback: if the library is missing or fails to load, every call raises.
+No fallback: if a library is missing or fails to load, every call of it raises.
 """
 from __future__ import annotations
 
@@ -80,6 +81,23 @@ def load() -> C.CDLL:
     L.pw_chunk_attn.restype = i
     _lib = L
     return L
+
+
+_binding = None
+
+
+def binding():
+    """The module _pw_binding; raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _pw_binding
+        except ImportError as e:
+            raise RuntimeError("_pw_binding.so is missing or does not load; build it with "
+                               "`python -m dynamic_sparse_attention_pw_b200.build`") from e
+        _binding = _pw_binding
+    return _binding
 
 
 def status_string(code: int) -> str:

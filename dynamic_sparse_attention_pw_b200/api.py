@@ -1,6 +1,8 @@
 """Python binding of the PageWeaver hot path (argument marshalling only).
 
-Every step of the path runs in libpw.so's kernels; torch supplies device memory and streams.
+Every step of the path runs in libpw.so's kernels; torch supplies device memory and streams.  The
+calls on new tokens are marshalled by a compiled module (csrc/pw_binding.cpp), which also checks
+their tensors.
 Names follow the C ABI (include/pw.h): pw_groups_size, pw_group, pw_attn.  `prefill` runs one
 complete call (pw_group then pw_attn on the current stream).  For new tokens over the paged cache:
 pw_qk_norm_rope, pw_append, pw_chunk_attn; `extend` runs the three in a row.
@@ -190,82 +192,12 @@ def prefill(Q, K_pages, V_pages, page_table, sel_pages, cu_seqlens, cu_seqlens_h
 # New tokens over the paged cache
 # ---------------------------------------------------------------------------------------
 
-def _run_on(device: torch.device, stream, fn, where: str, *args):
-    """fn(*args, stream) with `device` current: on `stream`, or on the device's current stream."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        code = fn(*args, s.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            code = fn(*args, s.cuda_stream)
-    if code != _lib.PW_OK:
-        raise PwError(code, where)
-
-
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """A tensor whose memory belongs to the stream the call runs on."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _rows(x: torch.Tensor | None, name: str, device, T=None):
-    """(pointer, token stride, head stride, heads) of bf16 rows of heads [T, H, 128]."""
-    if x is None:
-        return None, 0, 0, 0
-    n, H, D = x.shape
-    assert x.dtype is torch.bfloat16 and D == 128 and x.device == device, name
-    st, sh, sd = x.stride()
-    assert sd == 1 and (T is None or n == T), name
-    return x.data_ptr(), st if n > 1 else 128 * H, sh if H > 1 else 128, H
-
-
-def _batch(cu_seqlens: torch.Tensor, ctx_lens: torch.Tensor | None, device):
-    """(cu_seqlens, ctx_lens, B) of a batch of new tokens."""
-    assert cu_seqlens.dtype is torch.int32 and cu_seqlens.device == device and cu_seqlens.is_contiguous()
-    B = cu_seqlens.numel() - 1
-    if ctx_lens is None:
-        return cu_seqlens.data_ptr(), None, B
-    assert ctx_lens.dtype is torch.int32 and ctx_lens.device == device and ctx_lens.is_contiguous()
-    assert ctx_lens.numel() == B
-    return cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B
-
-
-def _weight(w: torch.Tensor | None, heads: int, device):
-    """(pointer, head stride) of a norm weight, bf16 [128] or [heads, 128]."""
-    if w is None:
-        return None, 0
-    assert w.dtype is torch.bfloat16 and w.device == device and w.is_contiguous()
-    assert tuple(w.shape) in ((128,), (heads, 128)), "norm weight: [128] or [heads, 128]"
-    return w.data_ptr(), 128 * (w.dim() - 1)
-
-
-def _rope(rope: torch.Tensor | None, device):
-    """(pointer, max_pos, rot_dim) of a rotation table."""
-    if rope is None:
-        return None, 0, 0
-    assert rope.dtype is torch.float32 and rope.dim() == 2 and rope.device == device
-    assert rope.is_contiguous()
-    return rope.data_ptr(), rope.shape[0], rope.shape[1]
-
-
-def _cache(K_pages: torch.Tensor, V_pages: torch.Tensor, page_table: torch.Tensor, B: int, device):
-    """(n_phys, Hkv) of a paged cache, checked against its page table."""
-    n_phys, Hkv, page, D = K_pages.shape
-    assert K_pages.dtype is torch.uint8 and V_pages.dtype is torch.uint8 and (page, D) == (64, 128)
-    assert K_pages.shape == V_pages.shape and K_pages.is_contiguous() and V_pages.is_contiguous()
-    assert K_pages.device == device and V_pages.device == device and page_table.device == device
-    assert page_table.dtype is torch.int32 and page_table.is_contiguous()
-    assert page_table.dim() == 2 and page_table.shape[0] == B
-    return n_phys, Hkv
-
-
-def _opt_ptr(t: torch.Tensor | None, dtype, device):
-    if t is None:
-        return None
-    assert t.dtype is dtype and t.device == device and t.is_contiguous()
-    return t.data_ptr()
 
 
 def rope_table(max_pos: int, rot_dim: int = 128, base: float = 10000.0,
@@ -292,21 +224,14 @@ def pw_qk_norm_rope(Q: torch.Tensor | None, K: torch.Tensor | None, cu_seqlens: 
     pw_qk_norm_rope).  Q bf16 [T, Hq, 128] and K bf16 [T, Hk, 128], views of a packed projection
     included, or either None; q_weight / k_weight bf16 [128] or [heads, 128] (None: no norm); rope
     from rope_table (None: no rotation).  Q_out = Q works in place.  Returns (Q_out, K_out)."""
-    L = _lib.load()
-    x = Q if Q is not None else K
-    assert x is not None and x.is_cuda
-    dev, T = x.device, x.shape[0]
-    q, k = _rows(Q, "Q", dev, T), _rows(K, "K", dev, T)
     if Q is not None and Q_out is None:
-        Q_out = _empty(Q.shape, Q.dtype, dev, stream)
+        Q_out = _empty(Q.shape, Q.dtype, Q.device, stream)
     if K is not None and K_out is None:
-        K_out = _empty(K.shape, K.dtype, dev, stream)
-    qo, ko = _rows(Q_out, "Q_out", dev, T), _rows(K_out, "K_out", dev, T)
-    assert qo[3] == q[3] and ko[3] == k[3], "an output's heads differ from its input's"
-    cu, ctx, B = _batch(cu_seqlens, ctx_lens, dev)
-    _run_on(dev, stream, L.pw_qk_norm_rope, "pw_qk_norm_rope", *q, *k, *_weight(q_weight, q[3], dev),
-            *_weight(k_weight, k[3], dev), eps, *_rope(rope, dev), interleaved, cu, ctx, B, T,
-            *qo[:3], *ko[:3], _opt_ptr(status, torch.int32, dev))
+        K_out = _empty(K.shape, K.dtype, K.device, stream)
+    code = _lib.binding().pw_qk_norm_rope(Q, K, cu_seqlens, ctx_lens, q_weight, k_weight, eps, rope,
+                                          interleaved, Q_out, K_out, status, stream)
+    if code:
+        raise PwError(code, "pw_qk_norm_rope")
     return Q_out, K_out
 
 
@@ -320,17 +245,10 @@ def pw_append(K: torch.Tensor, V: torch.Tensor, K_pages: torch.Tensor, V_pages: 
     bf16 [T, Hkv, 128], views of a packed projection included; the keys' norm (k_weight) and
     rotation (rope) happen on the way.  K_pages/V_pages uint8 [n_phys, Hkv, 64, 128]; page_table
     int32 [B, max_pages]."""
-    L = _lib.load()
-    assert K.is_cuda
-    dev, T = K.device, K.shape[0]
-    k, v = _rows(K, "K", dev), _rows(V, "V", dev, T)
-    cu, ctx, B = _batch(cu_seqlens, ctx_lens, dev)
-    n_phys, Hkv = _cache(K_pages, V_pages, page_table, B, dev)
-    assert k[3] == Hkv and v[3] == Hkv, "K and V have the cache's heads"
-    _run_on(dev, stream, L.pw_append, "pw_append", *k[:3], *v, *_weight(k_weight, Hkv, dev), eps,
-            *_rope(rope, dev), interleaved, cu, ctx, B, T, page_table.data_ptr(),
-            page_table.shape[1], n_phys, k_scale, v_scale, K_pages.data_ptr(), V_pages.data_ptr(),
-            _opt_ptr(status, torch.int32, dev))
+    code = _lib.binding().pw_append(K, V, K_pages, V_pages, page_table, cu_seqlens, ctx_lens, k_scale,
+                                    v_scale, k_weight, eps, rope, interleaved, status, stream)
+    if code:
+        raise PwError(code, "pw_append")
 
 
 def chunk_workspace(B: int, T: int, Hq: int, Hkv: int, max_q_len: int | None = None,
@@ -355,30 +273,23 @@ def pw_chunk_attn(Q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
     chunk (default T; any value is right, the true one is fastest); window > 0 limits each token to
     its last `window` keys; lse fp32 [T, Hq] receives the log-sum-exp of the scores.  Returns
     O bf16 [T, Hq, 128]."""
-    L = _lib.load()
-    assert Q.is_cuda
-    dev, T = Q.device, Q.shape[0]
-    q = _rows(Q, "Q", dev)
-    cu, ctx, B = _batch(cu_seqlens, ctx_lens, dev)
-    n_phys, Hkv = _cache(K_pages, V_pages, page_table, B, dev)
-    Hq = q[3]
+    T, Hq, D = Q.shape
     if max_q_len is None:
         max_q_len = max(T, 1)
     if sm_scale is None:
         sm_scale = 0.08838834764831845  # 1 / sqrt(128)
     if O is None:
-        O = _empty((T, Hq, 128), torch.bfloat16, dev, stream)
-    assert O.shape == Q.shape and (lse is None or tuple(lse.shape) == (T, Hq))
+        O = _empty((T, Hq, D), torch.bfloat16, Q.device, stream)
     if workspace is None:
         n = C.c_size_t()
-        _check(L.pw_chunk_workspace_size(B, T, Hq, Hkv, max_q_len, C.byref(n)), "pw_chunk_attn")
-        workspace = _empty(n.value, torch.uint8, dev, stream)
-    assert workspace.device == dev and workspace.is_contiguous()
-    _run_on(dev, stream, L.pw_chunk_attn, "pw_chunk_attn", *q, K_pages.data_ptr(), V_pages.data_ptr(),
-            Hkv, page_table.data_ptr(), page_table.shape[1], n_phys, cu, ctx, B, T, max_q_len,
-            window, k_scale, v_scale, sm_scale, _opt_ptr(O, torch.bfloat16, dev),
-            _opt_ptr(lse, torch.float32, dev), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _opt_ptr(status, torch.int32, dev))
+        _check(_lib.load().pw_chunk_workspace_size(cu_seqlens.numel() - 1, T, Hq, K_pages.shape[1],
+                                                   max_q_len, C.byref(n)), "pw_chunk_attn")
+        workspace = _empty(n.value, torch.uint8, Q.device, stream)
+    code = _lib.binding().pw_chunk_attn(Q, K_pages, V_pages, page_table, cu_seqlens, ctx_lens, max_q_len,
+                                        window, k_scale, v_scale, sm_scale, O, lse, workspace, status,
+                                        stream)
+    if code:
+        raise PwError(code, "pw_chunk_attn")
     return O
 
 

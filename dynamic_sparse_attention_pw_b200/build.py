@@ -1,16 +1,21 @@
-"""Build libpw.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc."""
+"""Build libpw.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and _pw_binding.so (its
+argument marshalling for the calls that a decoding step makes) with g++ against torch's headers."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libpw.so")
+BINDING_SRC = os.path.join(CSRC, "pw_binding.cpp")
+BINDING = os.path.join(HERE, "_pw_binding.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -37,20 +42,41 @@ def deps():
         [os.path.join(ROOT, "include", "pw.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target: str, sources) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in sources)
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and up_to_date():
-        return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", LIB, *sources()]
+def up_to_date() -> bool:
+    return _newer(LIB, deps())
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pw.h")]):
+        return BINDING
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *[f"-isystem{i}" for i in inc], BINDING_SRC, "-o", BINDING,
+           "-L" + HERE, "-l:libpw.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
+    return BINDING
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    if force or not up_to_date():
+        cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", LIB, *sources()]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+    build_binding(verbose=verbose)
     return LIB
 
 
