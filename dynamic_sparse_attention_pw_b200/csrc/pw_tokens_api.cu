@@ -62,8 +62,8 @@ pw_status check_batch(const int32_t *cu, int B, int64_t T)
     return T < (int64_t(1) << 31) ? PW_OK : PW_ERR_UNSUPPORTED;
 }
 
-// One warp takes at least one head of a token, eight warps a block.
-bool grid_fits(int64_t T, int64_t heads) { return T * heads < (int64_t(1) << 33); }
+// The second dimension of the grid counts heads by four.
+bool grid_fits(int64_t heads) { return heads <= 4 * 32767; }
 
 #define PW_TRY(x)                                                                                  \
     do {                                                                                           \
@@ -94,7 +94,7 @@ pw_status pw_qk_norm_rope(const void *Q, int64_t q_stride_t, int64_t q_stride_h,
     PW_TRY(check_rope(rope, max_pos, rot_dim));
     if (T == 0)
         return PW_OK;
-    if (!grid_fits(T, Hq + static_cast<int64_t>(Hk)))
+    if (!grid_fits(Hq + static_cast<int64_t>(Hk)))
         return PW_ERR_UNSUPPORTED;
     PW_TRY(check_in(Q, q_stride_t, q_stride_h, Hq));
     PW_TRY(check_in(K, k_stride_t, k_stride_h, Hk));
@@ -131,7 +131,7 @@ pw_status pw_append(const void *K, int64_t k_stride_t, int64_t k_stride_h, const
     PW_TRY(check_rope(rope, max_pos, rot_dim));
     if (T == 0)
         return PW_OK;
-    if (!grid_fits(T, 2 * static_cast<int64_t>(Hkv)))
+    if (!grid_fits(2 * static_cast<int64_t>(Hkv)))
         return PW_ERR_UNSUPPORTED;
     PW_TRY(check_in(K, k_stride_t, k_stride_h, Hkv));
     PW_TRY(check_in(V, v_stride_t, v_stride_h, Hkv));
