@@ -1,6 +1,5 @@
 // pw_chunk.cu -- pw_chunk_attn: causal attention of new tokens over the paged E4M3 cache; which
 // kernel a call takes, and what they need from the host.
-#include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -74,10 +73,8 @@ cudaError_t chunk_launch(const ChunkLaunch &launch, cudaStream_t st)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    const int ctas = std::min(sms, chunk::kMaxCtas);
-    L.ctas_mul = ~0ull / ctas + 1; // of no use, and not used, for one CTA
     const int64_t rows = rows_of(L.Hq, L.Hkv, L.max_q_len);
-    return rows <= kFewRows ? chunk::decode_launch(L, static_cast<int>(rows), ctas, st) : chunk::tiles_launch(L, ctas, st);
+    return rows <= kFewRows ? chunk::decode_launch(L, static_cast<int>(rows), sms, st) : chunk::tiles_launch(L, sms, st);
 }
 
 } // namespace pw

@@ -29,7 +29,10 @@ namespace chunk {
 using namespace tokens;
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
-constexpr int kMaxCtas = 148;  // one CTA per SM
+constexpr int kSms = 148;
+// CTAs of a kernel: small tiles two an SM, large ones one.
+template <int NT>
+__host__ __device__ constexpr int max_ctas() { return NT <= 32 ? 2 * kSms : kSms; }
 constexpr int kBlock = 128;    // keys per block
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
 
@@ -188,10 +191,10 @@ struct Cut {
 template <int NT>
 __host__ __device__ constexpr size_t partial_floats() { return static_cast<size_t>(NT) * (kHeadDim + 2); }
 
-constexpr size_t kCutBytes = (sizeof(Cut) * kMaxCtas + 255) / 256 * 256;
+constexpr size_t kCutBytes = (sizeof(Cut) * 2 * kSms + 255) / 256 * 256;
 
 template <int NT>
-__host__ __device__ constexpr size_t workspace_bytes() { return kCutBytes + 2 * kMaxCtas * partial_floats<NT>() * sizeof(float); }
+__host__ __device__ constexpr size_t workspace_bytes() { return kCutBytes + 2 * max_ctas<NT>() * partial_floats<NT>() * sizeof(float); }
 
 // Partial of CTA j, slot s: acc [NT][128], then max [NT], then sum [NT].
 template <int NT>
@@ -488,9 +491,9 @@ __device__ __forceinline__ int phys_slot(const ChunkLaunch &L, int b, int page)
 // swizzle, so that one copy lands a page as a matrix operand.
 cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap *map);
 
-cudaError_t decode_launch(const ChunkLaunch &L, int rows, int ctas, cudaStream_t st);
+cudaError_t decode_launch(ChunkLaunch &L, int rows, int sms, cudaStream_t st);
 size_t decode_workspace(int rows);
-cudaError_t tiles_launch(const ChunkLaunch &L, int ctas, cudaStream_t st);
+cudaError_t tiles_launch(ChunkLaunch &L, int sms, cudaStream_t st);
 size_t tiles_workspace();
 
 // Joins the partial results of the tiles that were cut: block j does the tile that stretch j starts
@@ -573,6 +576,15 @@ __global__ void __launch_bounds__(128, NT <= 32 ? 16 : 8) k_chunk_merge(const Ch
 
 // Lets k_chunk_merge come up; every thread of the attention kernels calls it.
 __device__ __forceinline__ void allow_merge() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// CTAs of the attention kernel on a device of that many SMs; sets what divides by it.
+template <int NT>
+int ctas_for(ChunkLaunch &L, int sms)
+{
+    const int ctas = (sms < kSms ? sms : kSms) * (max_ctas<NT>() / kSms);
+    L.ctas_mul = ~0ull / ctas + 1; // of no use, and not used, for one CTA
+    return ctas;
+}
 
 template <int NT>
 cudaError_t merge_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)

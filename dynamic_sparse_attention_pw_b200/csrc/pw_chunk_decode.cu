@@ -17,18 +17,16 @@
 // 2^-20 of it.  That costs one vote per block instead of a reduction over the keys, which lie along
 // the threads here.
 //
-// Two groups of eight softmax warps take blocks in turn (block c goes to group c % 2), each with its
-// own S, P, accumulator, reference and sums; they meet at the end of a tile.  The two warps of a
-// group that share a quarter of the keys share its rows: four of every eight each.  Sixteen warps
-// because the chain of a block is latency, not issue: with four warps a group it took 2600 cycles
-// for every eight rows.  Code that a tile runs once (its first block, its end) is kept short: at the
-// start of a call it runs from a cold instruction cache, and unrolled over the rows it alone took
-// 14 us.
+// Two CTAs share an SM, each with its own stretch of the work, so that one computes while the other
+// starts or ends a tile.  The two softmax warps that share a quarter of the keys share the rows: four of
+// every eight each, and the halves never wait for each other.  Code that a tile runs once (its first
+// block, its end) is kept short: at the start of a call it runs from a cold instruction cache, and
+// unrolled over the rows it alone took 14 us.
 //
-//   warp 0       load: page ids, TMA copies into the ring of K and V stages, job records
-//   warp 1       the products
-//   warps 2-3    the next tile's queries
-//   warps 4-19   softmax (two groups), and the end of a tile
+//   warps 0-7    softmax, and the end of a tile
+//   warp 8       load: page ids, TMA copies into the ring of K and V stages, job records
+//   warp 9       the products
+//   warp 10      the next tile's queries
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -41,37 +39,36 @@ namespace pw {
 namespace chunk {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kSoftmax = 512;  // threads of the softmax warps
+constexpr int kThreads = 352;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpQ = 10;
 constexpr int kJobs = 4;
-// Query tiles: S runs up to two blocks, so up to two tiles, ahead of the products, and a tile's slot is
+// Query tiles: S runs up to one block, so up to one tile, ahead of the products, and a tile's slot is
 // free when its results are written.
-constexpr int kQ = 3;
-constexpr uint32_t kBarAll = 5; // named barrier of all softmax warps (the groups' halves: 1 to 4)
+constexpr int kQ = 2;
 constexpr float kAbove = 4.f;  // a row's reference moves to this much above its largest score (base 2)
 
-template <int NT> constexpr int kStagesFor = NT == 16 ? 6 : 5;
+template <int NT> constexpr int kStagesFor = NT == 16 ? 3 : 2;
 
 template <int NT>
 struct __align__(1024) DecSmem {
     static constexpr int kStages = kStagesFor<NT>;
     uint8_t k[kStages][kBlock * 128]; // 128 keys x 128 dims
     uint8_t v[kStages][kBlock * 128];
-    // [group]: the weights as a matrix of 3 NT columns (part, row) by 128 keys, columns contiguous:
-    // cores of 8 keys by 16 columns (128 bytes), the cores of the same 8 keys side by side
-    uint8_t p[2][3 * NT * 128];
+    // the weights as a matrix of 3 NT columns (part, row) by 128 keys, columns contiguous: cores of
+    // 8 keys by 16 columns (128 bytes), the cores of the same 8 keys side by side
+    uint8_t p[3 * NT * 128];
     uint8_t q[kQ][2 * NT * 128];      // [tile % kQ][part, row][dim]
     float c[kQ][NT];                  // [tile % kQ]: factor of a row's scores
     int pos[kQ][NT];                  // [tile % kQ]: position of the row's token
     int at[kQ][NT];                   // [tile % kQ]: its row of O and lse
-    float nm[2][NT];                  // [group]: a row's reference, negated
-    float alpha[2][NT];               // [group]: factor when it moves
-    float red[2][4][NT];              // [group][key quarter]: block maxima, row sums
+    float nm[NT];                     // a row's reference, negated
+    float alpha[NT];                  // factor when it moves
+    float red[4][NT];                 // [key quarter]: block maxima, row sums
     Job job[kJobs];
     uint64_t job_full[kJobs], job_empty[kJobs];
     uint64_t q_full[kQ], q_empty[kQ];
     uint64_t k_full[kStages], v_full[kStages], st_empty[kStages];
-    uint64_t s_done[2], s_free[2], p_ready[2], pv_done[2];
+    uint64_t s_done[2], s_free[2], p_ready, pv_done;
     uint64_t drain;
     uint32_t issued; // blocks whose copies were issued
     uint32_t tmem;
@@ -106,11 +103,6 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4])
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t (&r)[2])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
-}
-
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
@@ -118,24 +110,19 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
 }
 
 // Waits for this thread's tcgen05.ld; the registers pass through it, so that no use moves before.
-template <int N>
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[4])
 {
-    static_assert(N == 2 || N == 4, "");
-    if (N == 2)
-        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1])::"memory");
-    else
-        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[N - 2]), "+r"(r[N - 1])::"memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     k_chunk_decode(const ChunkLaunch L, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
 {
     using Smem = DecSmem<NT>;
     constexpr int kSt = Smem::kStages;
-    constexpr uint32_t kTmemCols = NT == 16 ? 256 : 512;
-    constexpr uint32_t kColO = 4 * NT; // S of the two groups, then their accumulators
+    constexpr uint32_t kTmemCols = NT == 16 ? 128 : 256;
+    constexpr uint32_t kColO = 4 * NT; // two S, then the accumulator
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 2 * NT);
     constexpr uint32_t kIdescO = idesc_e4m3_f32(128, 3 * NT) | (1u << 15) | (1u << 16); // A (V^T) and B (P) MN-major
     constexpr int kKeys8 = 3 * NT * 8; // bytes of P of 8 keys
@@ -147,17 +134,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kJobs; ++i) {
             mbar_init(&sm.job_full[i], 1);
-            mbar_init(&sm.job_empty[i], 2 + 1 + 16); // query, product and softmax warps
+            mbar_init(&sm.job_empty[i], 1 + 1 + 8); // query, product and softmax warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_done[i], 1);
             mbar_init(&sm.s_free[i], 8);
-            mbar_init(&sm.p_ready[i], 8);
-            mbar_init(&sm.pv_done[i], 1);
         }
+        mbar_init(&sm.p_ready, 8);
+        mbar_init(&sm.pv_done, 1);
         for (int i = 0; i < kQ; ++i) {
-            mbar_init(&sm.q_full[i], 2);
-            mbar_init(&sm.q_empty[i], 1 + 16); // products, softmax warps
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1 + 8); // products, softmax warps
         }
         for (int i = 0; i < kSt; ++i) {
             mbar_init(&sm.k_full[i], 1);
@@ -169,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kWarpMma) {
         tmem_alloc(&sm.tmem, kTmemCols);
         tmem_relinquish();
     }
@@ -180,188 +167,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t *const ab = &sm.abort_flag;
     const Shape shape(L);
 
-    if (warp == 0) {
-        // ---------------- load ----------------
-        Pieces<NT> pieces;
-        pieces.begin(L, shape, cta, lane);
-        // slots of the 32 pages of job j from block k on, one a lane
-        auto fetch = [&](const Job &j, int k) {
-            const int pg = 2 * (j.blk0 + k) + lane; // between the pages that hold a key of the tile
-            return pg >= (j.lo >> 6) && pg <= ((j.hi - 1) >> 6) && pg < 2 * (j.blk0 + j.nblk) ? phys_slot(L, j.b, pg) : -1;
-        };
-        uint32_t c = 0;
-        Job j;
-        bool more = pieces.next(L, shape, cta, lane, j), ok = true;
-        int ids = more ? fetch(j, 0) : -1;
-        for (uint32_t n = 0; ok; ++n) {
-            ok = warp_wait(&sm.job_empty[n % kJobs], ((n / kJobs) & 1u) ^ 1u, ab);
-            if (!ok)
-                break;
-            if (!more)
-                j.nblk = -1;
-            if (lane == 0) {
-                sm.job[n % kJobs] = j;
-                mbar_arrive(&sm.job_full[n % kJobs]);
-            }
-            if (!more)
-                break;
-            Job jn;
-            int ids_n = -1, nxt = j.nblk > 16 ? fetch(j, 16) : -1;
-            // the next job is formed, and its first page ids asked for, while copies are in flight
-            const int ahead = min(j.nblk, kSt) - 1;
-            for (int k = 0; k < j.nblk; ++k, ++c) {
-                if (k > 0 && (k & 15) == 0) {
-                    ids = nxt;
-                    if (k + 16 < j.nblk)
-                        nxt = fetch(j, k + 16);
-                }
-                const int s0 = __shfl_sync(kFull, ids, 2 * (k & 15)), s1 = __shfl_sync(kFull, ids, 2 * (k & 15) + 1);
-                const uint32_t s = c % kSt;
-                ok = warp_wait(&sm.st_empty[s], ((c / kSt) & 1u) ^ 1u, ab);
-                if (!ok)
-                    break;
-                if (lane == 0) {
-                    const uint32_t bytes = ((s0 >= 0) + (s1 >= 0)) * attn::kPageBytes;
-                    const int y0 = (s0 * L.Hkv + j.h) * kPageTokens, y1 = (s1 * L.Hkv + j.h) * kPageTokens;
-                    mbar_arrive_expect_tx(&sm.k_full[s], bytes);
-                    if (s0 >= 0)
-                        tma_load_2d(sm.k[s], &map_k, 0, y0, &sm.k_full[s]);
-                    if (s1 >= 0)
-                        tma_load_2d(sm.k[s] + attn::kPageBytes, &map_k, 0, y1, &sm.k_full[s]);
-                    mbar_arrive_expect_tx(&sm.v_full[s], bytes);
-                    if (s0 >= 0)
-                        tma_load_2d(sm.v[s], &map_v, 0, y0, &sm.v_full[s]);
-                    if (s1 >= 0)
-                        tma_load_2d(sm.v[s] + attn::kPageBytes, &map_v, 0, y1, &sm.v_full[s]);
-                    sm.issued = c + 1;
-                }
-                __syncwarp();
-                if (k == ahead) {
-                    more = pieces.next(L, shape, cta, lane, jn);
-                    if (more)
-                        ids_n = fetch(jn, 0);
-                }
-            }
-            j = jn;
-            ids = ids_n;
-        }
-    } else if (warp == 1) {
-        // ---------------- products ----------------
-        // S of block c goes out before the products of block c - 2, the last block of the same group,
-        // also across the end of a tile: its S is read by then, so it computes while that group forms
-        // its weights.
-        const uint64_t dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024), dv = sdesc_sw128(smem_u32(sm.v[0]), 16, 1024);
-        const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dp = sdesc_plain(smem_u32(sm.p[0]), kKeys8, 128);
-        uint32_t c = 0;
-        bool ok = true;
-        // products of block cc, the first of its group in the tile or not
-        auto pv = [&](uint32_t cc, bool first) {
-            const uint32_t g = cc & 1u, s = cc % kSt;
-            if (!warp_wait(&sm.v_full[s], (cc / kSt) & 1u, ab) || !warp_wait(&sm.p_ready[g], (cc >> 1) & 1u, ab))
-                return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f8_ss(tmem + kColO + g * 3 * NT, dv + ((s * kBlock * 128 + kk * 32 * 128) >> 4),
-                              dp + ((g * 3 * NT * 128 + kk * 4 * kKeys8) >> 4), kIdescO, kk > 0 || !first);
-                mma_commit(&sm.pv_done[g]);
-                mma_commit(&sm.st_empty[s]);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool f1 = false, f2 = false; // blocks c - 1 and c - 2 are the first of their group in a tile
-        for (uint32_t n = 0; ok; ++n) {
-            ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
-            if (!ok)
-                break;
-            const int nblk = sm.job[n % kJobs].nblk;
-            warp_arrive(&sm.job_empty[n % kJobs], lane);
-            const uint32_t qb = n % kQ;
-            if (nblk >= 0)
-                ok = warp_wait(&sm.q_full[qb], (n / kQ) & 1u, ab);
-            // behind the last job: the products that are left
-            for (int k = 0; ok && k < (nblk >= 0 ? nblk : 2); ++k, ++c) {
-                if (nblk >= 0) {
-                    const uint32_t g = c & 1u, s = c % kSt;
-                    ok = warp_wait(&sm.k_full[s], (c / kSt) & 1u, ab) && warp_wait(&sm.s_free[g], ((c >> 1) & 1u) ^ 1u, ab);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f8_ss(tmem + g * 2 * NT, dk + ((s * kBlock * 128 + kk * 32) >> 4),
-                                      dq + ((qb * 2 * NT * 128 + kk * 32) >> 4), kIdescS, kk > 0);
-                        mma_commit(&sm.s_done[g]);
-                        if (k == nblk - 1)
-                            mma_commit(&sm.q_empty[qb]);
-                    }
-                    __syncwarp();
-                }
-                if (c >= 2)
-                    ok = pv(c - 2, f2);
-                f2 = f1;
-                f1 = k < 2;
-            }
-            if (nblk < 0)
-                break;
-        }
-    } else if (warp < 4) {
-        // ---------------- queries ----------------
-        const int half = lane >> 4, l = lane & 15;
-        for (uint32_t n = 0;; ++n) {
-            if (!warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab))
-                break;
-            const Job j = sm.job[n % kJobs];
-            warp_arrive(&sm.job_empty[n % kJobs], lane);
-            if (j.nblk < 0)
-                break;
-            const uint32_t qb = n % kQ;
-            if (!warp_wait(&sm.q_empty[qb], ((n / kQ) & 1u) ^ 1u, ab))
-                break;
-            // sixteen lanes a row, two rows of a half-warp at a time
-            for (int r0 = 2 * (warp - 2) + half; r0 < NT; r0 += 8) {
-                uint4 v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = r0 + 4 * i, flat = j.row + r, tok = shape.token(flat), head = j.h * L.G + flat - tok * L.G;
-                    const bool real = r < j.rows;
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (real)
-                        v[i] = __ldg(reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
-                                                                     static_cast<int64_t>(head) * L.q_sh) + l);
-                    if (l == 0) {
-                        sm.pos[qb][r] = real ? shape.position(j.ctx, tok) : -1;
-                        sm.at[qb][r] = (j.tok0 + tok) * L.Hq + head;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = r0 + 4 * i;
-                    const float c = stage_q_row(v[i], sm.q[qb], r, NT + r, l, L.score_scale);
-                    if (l == 0)
-                        sm.c[qb][r] = c;
-                }
-            }
-            fence_proxy_async_smem();
-            warp_arrive(&sm.q_full[qb], lane);
-        }
-    } else {
+    if (warp < kWarpLoad) {
         // ---------------- softmax ----------------
-        // A wait that fails is voted on at the next barrier of the group's half, so that its four warps
-        // leave together; a half that leaves, at the end of its work too, takes one turn at the barrier
-        // of all halves (kBarAll), where the others learn of it.
-        const uint32_t sub = (warp >> 2) - 1, g = sub >> 1, h4 = 4 * (sub & 1), bar = 1 + sub;
+        // A wait that fails is voted on at the next barrier of the half, so that its four warps leave
+        // together; the other half finds the abort flag.
+        const uint32_t h4 = 4 * (warp >> 2), bar = 1 + (warp >> 2);
         const int qd = warp & 3, key = 32 * qd + lane; // this thread's key of a block, and dim of O^T
         // its rows: 8 i + h4 + e, for e in 0..3 and i in 0..R8 - 1
         const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
-        const uint32_t s_addr = tmem + lanes + g * 2 * NT + h4, o_addr = tmem + lanes + kColO + h4;
-        uint8_t *const pcol = sm.p[g] + (key >> 3) * kKeys8 + (key & 7) * 16;
-        const float *const nm = sm.nm[g] + h4, *const alpha = sm.alpha[g] + h4;
+        const uint32_t o_addr = tmem + lanes + kColO + h4;
+        uint8_t *const pcol = sm.p + (key >> 3) * kKeys8 + (key & 7) * 16;
+        const float *const nm = sm.nm + h4, *const alpha = sm.alpha + h4;
         uint32_t c = 0; // blocks of the CTA before this tile
-        bool ok = true, left = false;
+        bool ok = true;
         for (uint32_t n = 0;; ++n) {
             ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
             if (bar_or(bar, 128, !ok))
@@ -374,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t qb = n % kQ;
             ok = warp_wait(&sm.q_full[qb], (n / kQ) & 1u, ab);
             if (key < NT && ((key ^ h4) & 4) == 0)
-                sm.nm[g][key] = key < rows ? -kNoMax : 0.f; // rows of padding score 0 and never move
+                sm.nm[key] = key < rows ? -kNoMax : 0.f; // rows of padding score 0 and never move
             if (bar_or(bar, 128, !ok))
                 break;
             const int R8 = (rows + 7) >> 3;                                 // groups of eight rows
@@ -384,13 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < NT / 8; ++i)
                 l[i][0] = l[i][1] = 0ull;
-            bool used = false, failed = false;
-            uint32_t u = 0;
-            for (int k = static_cast<int>((c ^ g) & 1u); k < nblk; k += 2, used = true) {
-                const uint32_t cc = c + k, s = cc % kSt;
-                u = cc >> 1;
+            bool failed = false;
+            for (int k = 0; k < nblk; ++k) {
+                const uint32_t cc = c + k, s = cc % kSt, g = cc & 1u, s_addr = tmem + lanes + g * 2 * NT + h4;
                 const int b0 = (blk0 + k) * kBlock, kp = b0 + key; // this thread's position
-                ok = warp_wait(&sm.s_done[g], u & 1u, ab);
+                ok = warp_wait(&sm.s_done[g], (cc >> 1) & 1u, ab);
                 tc_fence_after();
                 F2 y[NT / 8][2]; // base-2 exponents
                 bool over = false;
@@ -457,22 +273,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             unpack2(y[i][1], m.z, m.w);
                             m = make_float4(warp_max(m.x), warp_max(m.y), warp_max(m.z), warp_max(m.w));
                             if (lane == 0)
-                                *reinterpret_cast<float4 *>(&sm.red[g][qd][8 * i + h4]) = m;
+                                *reinterpret_cast<float4 *>(&sm.red[qd][8 * i + h4]) = m;
                         }
-                    if (ok && used) // the products so far
-                        ok = warp_wait(&sm.pv_done[g], (u - 1) & 1u, ab);
+                    if (ok && k > 0) // the products so far
+                        ok = warp_wait(&sm.pv_done, (cc - 1) & 1u, ab);
                     if (bar_or(bar, 128, !ok)) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
                     if (key < NT && ((key ^ h4) & 4) == 0) { // a thread a row
-                        const float top = fmaxf(fmaxf(sm.red[g][0][key], sm.red[g][1][key]), fmaxf(sm.red[g][2][key], sm.red[g][3][key]));
-                        const float m = sm.nm[g][key];
+                        const float top = fmaxf(fmaxf(sm.red[0][key], sm.red[1][key]), fmaxf(sm.red[2][key], sm.red[3][key]));
+                        const float m = sm.nm[key];
                         const bool move = key < rows && top + m > 0.f;
-                        sm.alpha[g][key] = move ? attn::ex2(-(top + kAbove) - m) : 1.f;
+                        sm.alpha[key] = move ? attn::ex2(-(top + kAbove) - m) : 1.f;
                         if (move)
-                            sm.nm[g][key] = -(top + kAbove);
+                            sm.nm[key] = -(top + kAbove);
                     }
                     bar_sync(bar, 128);
 #pragma unroll
@@ -482,13 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             l[i][0] = mul2(l[i][0], al.x);
                             l[i][1] = mul2(l[i][1], al.y);
                         }
-                    if (used) {
+                    if (k > 0) {
 #pragma unroll 1
                         for (int i = 0; i < R8; ++i) {
                             const float4 al = *reinterpret_cast<const float4 *>(alpha + 8 * i);
 #pragma unroll 1
                             for (int part = 0; part < 3; ++part) {
-                                const uint32_t at = o_addr + (g * 3 + part) * NT + 8 * i;
+                                const uint32_t at = o_addr + part * NT + 8 * i;
                                 uint32_t o[4];
                                 tmem_ld4(at, o);
                                 tmem_wait(o);
@@ -503,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                     }
                 }
-                // the group's last products have read its weights
-                if (cc >= 2)
-                    ok = warp_wait(&sm.pv_done[g], (u - 1) & 1u, ab);
+                // the last products have read their weights
+                if (cc >= 1)
+                    ok = warp_wait(&sm.pv_done, (cc - 1) & 1u, ab);
 #pragma unroll
                 for (int i = 0; i < NT / 8; ++i)
                     if (i < R8) {
@@ -539,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fence_proxy_async_smem();
-                warp_arrive(&sm.p_ready[g], lane);
+                warp_arrive(&sm.p_ready, lane);
             }
             if (failed)
                 break;
@@ -560,72 +376,216 @@ __global__ void __launch_bounds__(kThreads, 1)
                     z += __shfl_xor_sync(kFull, z, 2);
                     z += __shfl_xor_sync(kFull, z, 1);
                     if ((lane & 7) == 0)
-                        sm.red[g][qd][8 * i + h4 + (lane >> 3)] = z;
+                        sm.red[qd][8 * i + h4 + (lane >> 3)] = z;
                 }
-            if (ok && used)
-                ok = warp_wait(&sm.pv_done[g], u & 1u, ab);
-            tc_fence_before();
-            if (bar_or(kBarAll, kSoftmax, !ok)) {
-                left = true;
+            if (ok)
+                ok = warp_wait(&sm.pv_done, (c + nblk - 1) & 1u, ab);
+            if (bar_or(bar, 128, !ok))
                 break;
-            }
             tc_fence_after();
-            // Each half of a group joins the accumulators of both for two of its four rows.
             float *const part = slot >= 0 ? partial<NT>(L, cta, slot) : nullptr;
-            const bool both = nblk > 1;
 #pragma unroll 1
             for (int i = 0; i < R8; ++i) {
-                const int r = 8 * i + h4 + 2 * static_cast<int>(g); // rows r and r + 1
-                if (r >= rows)
-                    break;
-                float o[2][2];
+                const int r = 8 * i + h4; // rows r to r + 3
+                uint32_t x[4], y[4], z[4];
+                tmem_ld4(o_addr + 8 * i, x);
+                tmem_ld4(o_addr + NT + 8 * i, y);
+                tmem_ld4(o_addr + 2 * NT + 8 * i, z);
+                tmem_wait(x);
+                tmem_wait(y);
+                tmem_wait(z);
 #pragma unroll
-                for (int gg = 0; gg < 2; ++gg) {
-                    o[gg][0] = o[gg][1] = 0.f;
-                    if (both || static_cast<uint32_t>(gg) == (c & 1u)) { // the group has had a block
-                        const uint32_t at = o_addr + gg * 3 * NT + 8 * i + 2 * g;
-                        uint32_t x[2], y[2], z[2];
-                        tmem_ld2(at, x);
-                        tmem_ld2(at + NT, y);
-                        tmem_ld2(at + 2 * NT, z);
-                        tmem_wait(x);
-                        tmem_wait(y);
-                        tmem_wait(z);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            o[gg][e] = fmaf(fmaf(__uint_as_float(z[e]), 0x1p-4f, __uint_as_float(y[e])), 0x1p-4f, __uint_as_float(x[e])) * 0x1p-8f;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 4; ++e)
                     if (r + e < rows) {
                         const int rr = r + e;
-                        const float m0 = -sm.nm[0][rr], m1 = -sm.nm[1][rr], m = fmaxf(m0, m1);
-                        const float a0 = attn::ex2(m0 - m), a1 = attn::ex2(m1 - m);
-                        const float sum = a0 * ((sm.red[0][0][rr] + sm.red[0][1][rr]) + (sm.red[0][2][rr] + sm.red[0][3][rr])) +
-                                          a1 * ((sm.red[1][0][rr] + sm.red[1][1][rr]) + (sm.red[1][2][rr] + sm.red[1][3][rr]));
-                        const float v = a0 * o[0][e] + a1 * o[1][e];
+                        const float v = fmaf(fmaf(__uint_as_float(z[e]), 0x1p-4f, __uint_as_float(y[e])), 0x1p-4f, __uint_as_float(x[e])) * 0x1p-8f;
+                        const float sum = (sm.red[0][rr] + sm.red[1][rr]) + (sm.red[2][rr] + sm.red[3][rr]);
                         if (part != nullptr) {
                             part[rr * kHeadDim + key] = v;
                             if (key == 0) {
-                                part[NT * kHeadDim + rr] = m;
+                                part[NT * kHeadDim + rr] = -sm.nm[rr];
                                 part[NT * (kHeadDim + 1) + rr] = sum;
                             }
                         } else {
                             const int64_t at = sm.at[qb][rr];
                             L.O[at * kHeadDim + key] = __bfloat16_as_ushort(__float2bfloat16_rn(v * (L.v_scale / sum)));
                             if (L.lse != nullptr && key == 0)
-                                L.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
+                                L.lse[at] = (log2f(sum) - sm.nm[rr]) * 0.6931471805599453f;
                         }
                     }
             }
             tc_fence_before();
             warp_arrive(&sm.q_empty[qb], lane); // positions, places and factors read
-            bar_sync(kBarAll, kSoftmax);        // references, sums and accumulators read
+            bar_sync(bar, 128);                 // references and sums read
             c += nblk;
         }
-        if (!left)
-            (void)bar_or(kBarAll, kSoftmax, true);
+    } else if (warp == kWarpLoad) {
+        // ---------------- load ----------------
+        Pieces<NT> pieces;
+        pieces.begin(L, shape, cta, lane);
+        // slots of the 32 pages of job j from block k on, one a lane
+        auto fetch = [&](const Job &j, int k) {
+            const int pg = 2 * (j.blk0 + k) + lane; // between the pages that hold a key of the tile
+            return pg >= (j.lo >> 6) && pg <= ((j.hi - 1) >> 6) && pg < 2 * (j.blk0 + j.nblk) ? phys_slot(L, j.b, pg) : -1;
+        };
+        uint32_t c = 0;
+        Job j;
+        bool more = pieces.next(L, shape, cta, lane, j), ok = true;
+        int ids = more ? fetch(j, 0) : -1;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = warp_wait(&sm.job_empty[n % kJobs], ((n / kJobs) & 1u) ^ 1u, ab);
+            if (!ok)
+                break;
+            if (!more)
+                j.nblk = -1;
+            if (lane == 0) {
+                sm.job[n % kJobs] = j;
+                mbar_arrive(&sm.job_full[n % kJobs]);
+            }
+            if (!more)
+                break;
+            Job jn;
+            int ids_n = -1, nxt = j.nblk > 16 ? fetch(j, 16) : -1;
+            // the next job is formed, and its first page ids asked for, while copies are in flight
+            const int ahead = min(j.nblk, kSt) - 1;
+            for (int k = 0; k < j.nblk; ++k, ++c) {
+                if (k > 0 && (k & 15) == 0) {
+                    ids = nxt;
+                    if (k + 16 < j.nblk)
+                        nxt = fetch(j, k + 16);
+                }
+                const int s0 = __shfl_sync(kFull, ids, 2 * (k & 15)), s1 = __shfl_sync(kFull, ids, 2 * (k & 15) + 1);
+                const uint32_t s = c % kSt;
+                ok = warp_wait(&sm.st_empty[s], ((c / kSt) & 1u) ^ 1u, ab);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    const uint32_t bytes = ((s0 >= 0) + (s1 >= 0)) * attn::kPageBytes;
+                    const int y0 = (s0 * L.Hkv + j.h) * kPageTokens, y1 = (s1 * L.Hkv + j.h) * kPageTokens;
+                    mbar_arrive_expect_tx(&sm.k_full[s], bytes);
+                    if (s0 >= 0)
+                        tma_load_2d(sm.k[s], &map_k, 0, y0, &sm.k_full[s]);
+                    if (s1 >= 0)
+                        tma_load_2d(sm.k[s] + attn::kPageBytes, &map_k, 0, y1, &sm.k_full[s]);
+                    mbar_arrive_expect_tx(&sm.v_full[s], bytes);
+                    if (s0 >= 0)
+                        tma_load_2d(sm.v[s], &map_v, 0, y0, &sm.v_full[s]);
+                    if (s1 >= 0)
+                        tma_load_2d(sm.v[s] + attn::kPageBytes, &map_v, 0, y1, &sm.v_full[s]);
+                    sm.issued = c + 1;
+                }
+                __syncwarp();
+                if (k == ahead) {
+                    more = pieces.next(L, shape, cta, lane, jn);
+                    if (more)
+                        ids_n = fetch(jn, 0);
+                }
+            }
+            j = jn;
+            ids = ids_n;
+        }
+    } else if (warp == kWarpMma) {
+        // ---------------- products ----------------
+        // S of block c goes out before the products of block c - 1, also across the end of a tile, so
+        // that it is there when the softmax comes to it.
+        const uint64_t dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024), dv = sdesc_sw128(smem_u32(sm.v[0]), 16, 1024);
+        const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dp = sdesc_plain(smem_u32(sm.p), kKeys8, 128);
+        uint32_t c = 0;
+        bool ok = true;
+        // products of block cc, the first of its tile or not
+        auto pv = [&](uint32_t cc, bool first) {
+            const uint32_t s = cc % kSt;
+            if (!warp_wait(&sm.v_full[s], (cc / kSt) & 1u, ab) || !warp_wait(&sm.p_ready, cc & 1u, ab))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f8_ss(tmem + kColO, dv + ((s * kBlock * 128 + kk * 32 * 128) >> 4), dp + ((kk * 4 * kKeys8) >> 4), kIdescO,
+                              kk > 0 || !first);
+                mma_commit(&sm.pv_done);
+                mma_commit(&sm.st_empty[s]);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool f1 = false; // block c - 1 is the first of its tile
+        for (uint32_t n = 0; ok; ++n) {
+            ok = warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab);
+            if (!ok)
+                break;
+            const int nblk = sm.job[n % kJobs].nblk;
+            warp_arrive(&sm.job_empty[n % kJobs], lane);
+            const uint32_t qb = n % kQ;
+            if (nblk >= 0)
+                ok = warp_wait(&sm.q_full[qb], (n / kQ) & 1u, ab);
+            // behind the last job: the products that are left
+            for (int k = 0; ok && k < (nblk >= 0 ? nblk : 1); ++k, ++c) {
+                if (nblk >= 0) {
+                    const uint32_t g = c & 1u, s = c % kSt;
+                    ok = warp_wait(&sm.k_full[s], (c / kSt) & 1u, ab) && warp_wait(&sm.s_free[g], ((c >> 1) & 1u) ^ 1u, ab);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8_ss(tmem + g * 2 * NT, dk + ((s * kBlock * 128 + kk * 32) >> 4),
+                                      dq + ((qb * 2 * NT * 128 + kk * 32) >> 4), kIdescS, kk > 0);
+                        mma_commit(&sm.s_done[g]);
+                        if (k == nblk - 1)
+                            mma_commit(&sm.q_empty[qb]);
+                    }
+                    __syncwarp();
+                }
+                if (c >= 1)
+                    ok = pv(c - 1, f1);
+                f1 = k == 0;
+            }
+            if (nblk < 0)
+                break;
+        }
+    } else if (warp == kWarpQ) {
+        // ---------------- queries ----------------
+        const int half = lane >> 4, l = lane & 15;
+        for (uint32_t n = 0;; ++n) {
+            if (!warp_wait(&sm.job_full[n % kJobs], (n / kJobs) & 1u, ab))
+                break;
+            const Job j = sm.job[n % kJobs];
+            warp_arrive(&sm.job_empty[n % kJobs], lane);
+            if (j.nblk < 0)
+                break;
+            const uint32_t qb = n % kQ;
+            if (!warp_wait(&sm.q_empty[qb], ((n / kQ) & 1u) ^ 1u, ab))
+                break;
+            // sixteen lanes a row, four rows of a half-warp at a time
+#pragma unroll 1
+            for (int r0 = half; r0 < NT; r0 += 8) {
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + 2 * i, flat = j.row + r, tok = shape.token(flat), head = j.h * L.G + flat - tok * L.G;
+                    const bool real = r < j.rows;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (real)
+                        v[i] = __ldg(reinterpret_cast<const uint4 *>(L.Q + (static_cast<int64_t>(j.tok0) + tok) * L.q_st +
+                                                                     static_cast<int64_t>(head) * L.q_sh) + l);
+                    if (l == 0) {
+                        sm.pos[qb][r] = real ? shape.position(j.ctx, tok) : -1;
+                        sm.at[qb][r] = (j.tok0 + tok) * L.Hq + head;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + 2 * i;
+                    const float c = stage_q_row(v[i], sm.q[qb], r, NT + r, l, L.score_scale);
+                    if (l == 0)
+                        sm.c[qb][r] = c;
+                }
+            }
+            fence_proxy_async_smem();
+            warp_arrive(&sm.q_full[qb], lane);
+        }
     }
 
     tc_fence_before();
@@ -641,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 (void)mbar_wait(&sm.v_full[s], (last / kSt) & 1u);
             }
         }
-        if (warp == 1) {
+        if (warp == kWarpMma) {
             if (elect_one()) {
                 mma_commit(&sm.drain);
                 (void)mbar_wait(&sm.drain, 0);
@@ -650,16 +610,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
 }
 
 template <int NT>
-cudaError_t launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
+cudaError_t launch(ChunkLaunch &L, int sms, cudaStream_t st)
 {
-    static_assert(sizeof(DecSmem<NT>) + 1024 <= 227 * 1024, "shared-memory layout too large");
+    const int ctas = ctas_for<NT>(L, sms);
+    static_assert(sizeof(DecSmem<NT>) + 1024 <= 113 * 1024, "shared-memory layout too large");
     CUtensorMap k, v;
     cudaError_t e = page_tensor(L.K, L, &k);
     if (e == cudaSuccess)
@@ -667,6 +628,8 @@ cudaError_t launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
     const int smem = static_cast<int>(sizeof(DecSmem<NT>) + 1024);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_chunk_decode<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) // room for both CTAs of an SM
+        e = cudaFuncSetAttribute(k_chunk_decode<NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess)
         return e;
     k_chunk_decode<NT><<<ctas, kThreads, smem, st>>>(L, k, v);
@@ -678,9 +641,9 @@ cudaError_t launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
 
 size_t decode_workspace(int rows) { return rows <= 16 ? workspace_bytes<16>() : workspace_bytes<32>(); }
 
-cudaError_t decode_launch(const ChunkLaunch &L, int rows, int ctas, cudaStream_t st)
+cudaError_t decode_launch(ChunkLaunch &L, int rows, int sms, cudaStream_t st)
 {
-    return rows <= 16 ? launch<16>(L, ctas, st) : launch<32>(L, ctas, st);
+    return rows <= 16 ? launch<16>(L, sms, st) : launch<32>(L, sms, st);
 }
 
 } // namespace chunk

@@ -592,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 size_t tiles_workspace() { return workspace_bytes<kRows>(); }
 
-cudaError_t tiles_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
+cudaError_t tiles_launch(ChunkLaunch &L, int sms, cudaStream_t st)
 {
+    const int ctas = ctas_for<kRows>(L, sms);
     CUtensorMap k;
     cudaError_t e = page_tensor(L.K, L, &k);
     const int smem = static_cast<int>(sizeof(TileSmem) + 1024);
