@@ -499,9 +499,9 @@ size_t tiles_workspace();
 // Joins the partial results of the tiles that were cut: block j does the tile that stretch j starts
 // inside of, unless an earlier stretch starts inside of it too.  A warp has NT / 64 rows (one of a
 // small tile).  Where the attention kernel leaves registers (few rows), the blocks are brought up while
-// it still runs (programmatic launch) and wait for its end: 128 threads of 32 registers fit beside it.
+// it still runs (programmatic launch) and wait for its end: 128 threads of 64 registers fit beside it.
 template <int NT>
-__global__ void __launch_bounds__(128, NT <= 32 ? 16 : 8) k_chunk_merge(const ChunkLaunch L)
+__global__ void __launch_bounds__(128, 8) k_chunk_merge(const ChunkLaunch L)
 {
     constexpr int kR = NT <= 64 ? 1 : NT / 64;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(128, NT <= 32 ? 16 : 8) k_chunk_merge(const Ch
             }
         }
         const int m = min(32, n - i0);
-#pragma unroll(kR == 1 ? 4 : 1)
+#pragma unroll(kR == 1 ? 8 : 2)
         for (int i = 0; i < m; ++i) {
             const float4 *o = reinterpret_cast<const float4 *>(piece(i0 + i) + r0 * kHeadDim) + lane;
 #pragma unroll
