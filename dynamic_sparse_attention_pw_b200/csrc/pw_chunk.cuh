@@ -476,6 +476,17 @@ __device__ __forceinline__ float stage_q_row(const uint4 v, uint8_t *tile, int r
     return q_factor(e, score_scale);
 }
 
+// Bytes of w that hold the E4M3 code of NaN, as 0xFF each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu; }
+
+// Takes the NaN codes out of a chunk of values; whether there were any.
+__device__ __forceinline__ bool drop_nan(uint4 &x)
+{
+    const uint4 n = make_uint4(nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w));
+    x = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+    return (n.x | n.y | n.z | n.w) != 0u;
+}
+
 // Physical slot of a page, checked; 0 where the entry is bad (recorded).
 __device__ __forceinline__ int phys_slot(const ChunkLaunch &L, int b, int page)
 {

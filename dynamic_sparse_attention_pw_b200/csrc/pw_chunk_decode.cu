@@ -64,6 +64,7 @@ struct __align__(1024) DecSmem {
     float nm[NT];                     // a row's reference, negated
     float alpha[NT];                  // factor when it moves
     float red[4][NT];                 // [key quarter]: block maxima, row sums
+    float bad[kQ][NT];                // [tile % kQ]: NaN for a row that sees a value taken out as NaN, else 0
     Job job[kJobs];
     uint64_t job_full[kJobs], job_empty[kJobs];
     uint64_t q_full[kQ], q_empty[kQ];
@@ -107,6 +108,26 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
+}
+
+// One key's values without their NaN; the rows that see the key (position kp) get one.  Rare, and so not
+// inlined.
+static __device__ __noinline__ void take_nan(uint4 *row, int kp, const int *pos, float *bad, int rows, int window)
+{
+    bool has = false;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        uint4 x = row[i];
+        if (drop_nan(x)) {
+            row[i] = x;
+            has = true;
+        }
+    }
+    if (has)
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r)
+            if (pos[r] >= kp && (window == 0 || pos[r] - kp < window))
+                bad[r] = __int_as_float(0x7FC00000);
 }
 
 // Waits for this thread's tcgen05.ld; the registers pass through it, so that no use moves before.
@@ -236,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tc_fence_before();
                 warp_arrive(&sm.s_free[g], lane);
                 // some row does not see the whole block
-                if (b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window)) {
+                const bool edge = b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= pos_hi - L.window);
+                if (edge) {
 #pragma unroll
                     for (int i = 0; i < NT / 8; ++i)
                         if (i < R8) {
@@ -354,6 +376,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                             row[i] = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
+                // Nor where one token of the tile sees a key and another does not: there NaN leaves the
+                // values and enters the sums of the rows that see it.
+                if (h4 == 0 && edge && pos_lo != pos_hi) {
+                    ok = warp_wait(&sm.v_full[s], (cc / kSt) & 1u, ab) && ok;
+                    take_nan(reinterpret_cast<uint4 *>(sm.v[s] + key * 128), kp, sm.pos[qb], sm.bad[qb], rows, L.window);
+                }
                 fence_proxy_async_smem();
                 warp_arrive(&sm.p_ready, lane);
             }
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (r + e < rows) {
                         const int rr = r + e;
                         const float v = fmaf(fmaf(__uint_as_float(z[e]), 0x1p-4f, __uint_as_float(y[e])), 0x1p-4f, __uint_as_float(x[e])) * 0x1p-8f;
-                        const float sum = (sm.red[0][rr] + sm.red[1][rr]) + (sm.red[2][rr] + sm.red[3][rr]);
+                        const float sum = ((sm.red[0][rr] + sm.red[1][rr]) + (sm.red[2][rr] + sm.red[3][rr])) + sm.bad[qb][rr];
                         if (part != nullptr) {
                             part[rr * kHeadDim + key] = v;
                             if (key == 0) {
@@ -573,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (l == 0) {
                         sm.pos[qb][r] = real ? shape.position(j.ctx, tok) : -1;
                         sm.at[qb][r] = (j.tok0 + tok) * L.Hq + head;
+                        sm.bad[qb][r] = 0.f;
                     }
                 }
 #pragma unroll

@@ -42,6 +42,7 @@ struct __align__(1024) TileSmem {
     uint8_t v[kNV][kBlock * 128];   // E4M3 as stored
     uint8_t v16[2][2][kBlock * 128]; // [block % 2][dims 0-63, 64-127][key][dim] f16, swizzled
     float c[2][2][kHalf];           // [half][its tile % 2]: factor of a row's scores
+    float bad[2][2][kHalf];         // [half][its tile % 2]: NaN for a row that sees a value taken out as NaN, else 0
     Job job[kJobs];
     uint64_t job_full[kJobs], job_empty[kJobs];
     uint64_t q_full[2], q_empty[2];
@@ -127,6 +128,27 @@ static __device__ __noinline__ void rescale(uint32_t o_addr, int no, uint32_t p_
         tmem_st16(at, x);
     }
     tmem_st_wait();
+}
+
+// Takes the NaN out of the values of the block at b0 (the pieces that thread t converts); the rows of the
+// tile that see such a key get one.  Rare, and so not inlined.
+static __device__ __noinline__ void take_nan(uint8_t *v, int t, int b0, const Shape shape, int ctx, int row, int rows, float *bad0, float *bad1)
+{
+#pragma unroll 1
+    for (int q = t; q < kBlock * 8; q += 128) {
+        uint4 *const at = reinterpret_cast<uint4 *>(v + q * 16);
+        uint4 x = *at;
+        if (!drop_nan(x))
+            continue;
+        *at = x;
+        const int kp = b0 + (q >> 3);
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) {
+            const int pos = shape.position(ctx, shape.token(row + r));
+            if (pos >= kp && (shape.window == 0 || pos - kp < shape.window))
+                (r < kHalf ? bad0 : bad1)[r & (kHalf - 1)] = __int_as_float(0x7FC00000);
+        }
+    }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -285,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
             float l0, l1;
             unpack2(add2(l[0], l[1]), l0, l1);
-            const float sum = l0 + l1, inv = L.v_scale / sum;
+            const float sum = (l0 + l1) + sm.bad[a][nt & 1u][r & 127], inv = L.v_scale / sum;
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t o[32];
@@ -363,10 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4 *>(sm.q[a][1] + at) = make_uint4(a2.x, a2.y, b2.x, b2.y);
                 }
                 sm.c[a][nt[a] & 1u][t] = q_factor(e, L.score_scale);
+                sm.bad[a][nt[a] & 1u][t] = 0.f;
                 fence_proxy_async_smem();
                 warp_arrive(&sm.q_full[a], lane);
                 ++nt[a];
             }
+            const int pos_lo = shape.position(j.ctx, shape.token(j.row));
             for (int k = 0; ok && k < j.nblk; ++k, ++c) {
                 const uint32_t sv = c % kNV, slot = c & 1u;
                 ok = warp_wait(&sm.v_full[sv], (c / kNV) & 1u, ab) && warp_wait(&sm.v16_empty[slot], ((c >> 1) & 1u) ^ 1u, ab);
@@ -376,6 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // and zero times NaN is not zero: they enter as zeros.
                 const int b0 = (j.blk0 + k) * kBlock;
                 const bool edge = b0 < j.lo || b0 + kBlock > j.hi;
+                // Nor where one token of the tile sees a key and another does not: there NaN leaves the
+                // values and enters the sums of the rows that see it.
+                if (b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= j.hi - 1 - L.window))
+                    take_nan(sm.v[sv], t, b0, shape, j.ctx, j.row, j.rows, sm.bad[0][(nt[0] - 1) & 1u], sm.bad[1][(nt[1] - 1) & 1u]);
 #pragma unroll 2
                 for (int i = 0; i < 8; ++i) {
                     const int q = t + 128 * i, key = q >> 3, c16 = q & 7;

@@ -360,6 +360,34 @@ def test_chunk_attn_pages_outside_the_window_are_not_touched(q):
     ref.assert_bf16(O, want, bO)
 
 
+@pytest.mark.parametrize("q,ctx,window,max_q", [(5, 120, 0, 5), (8, 1000, 0, 8), (6, 300, 100, 6), (60, 0, 0, 60), (200, 500, 0, 200),
+                                                (150, 400, 90, 150), (70, 100, 0, 1)])
+@pytest.mark.parametrize("which", ["keys", "values"])
+def test_chunk_attn_nan_reaches_the_rows_that_see_it_alone(q, ctx, window, max_q, which):
+    """A NaN in the cache makes the tokens that attend to it NaN, and no other token of the chunk."""
+    rng = np.random.default_rng(16)
+    cu, cl, table, Q, Kp, Vp = _attn_inputs(rng, [q], [ctx], 8, 2)
+    clean = [Kp.copy(), Vp.copy()]
+    bad = [ctx + q // 2, ctx + q - 1] + ([max(0, ctx - window + 2)] if window else [])
+    for p in bad:
+        (Kp if which == "keys" else Vp)[table[0, p // 64], 1, p % 64, 7] = 0xFF
+    status = api.new_status(DEV)
+    kw = dict(max_q_len=max_q, k_scale=2.0 ** -6, v_scale=2.0 ** -6, window=window, status=status)
+    run = lambda K, V: api.pw_chunk_attn(Q, torch.from_numpy(K).to(DEV), torch.from_numpy(V).to(DEV), _i32(table),  # noqa: E731
+                                         _i32(cu), _i32(cl), **kw)
+    got = run(Kp, Vp)
+    _ok(status)
+    want, _, bO, _ = ref.attn(ref.f64(Q), *clean, table, [q], [ctx], 2.0 ** -6, 2.0 ** -6, 128 ** -0.5, window)
+    pos = ctx + np.arange(q)
+    sees = np.zeros(q, bool)
+    for p in bad:
+        sees |= (p <= pos) & ((window == 0) | (p > pos - window))
+    assert sees.any() and not sees.all()
+    assert bool(got[torch.from_numpy(sees).to(DEV), 4:, 7].isnan().all())  # kv head 1: query heads 4..7
+    ref.assert_bf16(got[:, :4], want[:, :4], bO[:, :4], "the other kv head")
+    ref.assert_bf16(got[torch.from_numpy(~sees).to(DEV)], want[~sees], bO[~sees], "rows that do not see it")
+
+
 def test_chunk_attn_same_bits_every_time_and_any_batch_order():
     rng = np.random.default_rng(15)
     for q in (1, 90):
