@@ -517,11 +517,14 @@ __global__ void __launch_bounds__(128, 8) k_chunk_merge(const ChunkLaunch L)
     constexpr int kR = NT <= 64 ? 1 : NT / 64;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int j = blockIdx.x, lane = threadIdx.x & 31, r0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * kR;
+    // Records are read as they lie there and never trusted for an address: where two calls share a
+    // workspace against the rules, the results are wrong, but nothing outside the buffers is touched.
     const Cut c = reinterpret_cast<const Cut *>(L.workspace)[j];
-    if (!c.inside || r0 >= c.rows || c.all.begin(j - 1) > c.ts)
+    const int ctas = min(c.all.ctas, static_cast<int>(gridDim.x)), rows = min(c.rows, NT);
+    if (c.inside != 1 || j == 0 || r0 >= rows || c.all.begin(j - 1) > c.ts)
         return;
     int n = 1; // pieces: slot 1 of CTA j - 1, slot 0 of CTAs j .. j + n - 2
-    while (j + n - 1 < c.all.ctas && c.all.begin(j + n - 1) < c.te)
+    while (j + n - 1 < ctas && c.all.begin(j + n - 1) < c.te)
         ++n;
     const float *first = partial<NT>(L, j - 1, 1), *rest = partial<NT>(L, j, 0);
     auto piece = [&](int i) { return i == 0 ? first : rest + static_cast<size_t>(i - 1) * 2 * partial_floats<NT>(); };
@@ -572,11 +575,13 @@ __global__ void __launch_bounds__(128, 8) k_chunk_merge(const ChunkLaunch L)
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             sum[e] += __shfl_xor_sync(kFull, sum[e], d);
-        if (r0 + e >= c.rows)
+        if (r0 + e >= rows)
             break;
         const float inv = L.v_scale / sum[e];
         const int flat = c.row + r0 + e, tok = Shape(L).token(flat);
-        const int64_t at = (static_cast<int64_t>(c.tok0) + tok) * L.Hq + c.h * L.G + flat - tok * L.G;
+        const int64_t at = (static_cast<int64_t>(c.tok0) + tok) * L.Hq + static_cast<int64_t>(c.h) * L.G + flat - tok * L.G;
+        if (at < 0 || at >= L.tb.T * L.Hq)
+            break;
         const __nv_bfloat162 a = __floats2bfloat162_rn(acc[e].x * inv, acc[e].y * inv), b = __floats2bfloat162_rn(acc[e].z * inv, acc[e].w * inv);
         reinterpret_cast<uint2 *>(L.O + at * kHeadDim)[lane] =
             make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));

@@ -185,7 +185,7 @@ pw_status pw_chunk_attn(const void *Q, int64_t q_stride_t, int64_t q_stride_h, i
         return PW_ERR_UNSUPPORTED; // positions, and cache rows, are addressed with 32 bits
     if (T == 0)
         return PW_OK;
-    if (T * static_cast<int64_t>(Hq) > 0x7FFFFFFFll)
+    if (T * static_cast<int64_t>(Hq) > 0x7FFFF000ll)
         return PW_ERR_UNSUPPORTED; // rows are counted with 32 bits
     PW_TRY(check_in(Q, q_stride_t, q_stride_h, Hq));
     if (!K_pages || !V_pages || !page_table || !O || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O))

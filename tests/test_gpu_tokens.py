@@ -279,6 +279,67 @@ def test_chunk_attn(qlens, ctx, Hq, Hkv, window, max_q_len):
     _check_attn(qlens, ctx, Hq, Hkv, window, max_q_len, seed=len(qlens) + Hq + window, pad=2)
 
 
+@pytest.mark.parametrize("qlens,ctx,max_q", [
+    ([1] * 300, [(7 * i) % 190 for i in range(300)], 1),                            # more sequences than are counted at once
+    ([1, 0, 0] * 100 + [0] * 40, [(11 * i) % 260 for i in range(340)], 1),
+    ([(3 * i) % 41 for i in range(150)], [(13 * i) % 150 for i in range(150)], 40),  # the same with large tiles
+    ([0] * 140 + [200], [5] * 141, 200),
+])
+def test_chunk_attn_many_sequences(qlens, ctx, max_q):
+    _check_attn(qlens, ctx, 16 if max_q > 1 else 8, 2, 0, max_q, seed=17, pad=1)
+
+
+@pytest.mark.parametrize("max_q", [1, 300])
+def test_chunk_attn_no_tokens_at_all(max_q):
+    rng = np.random.default_rng(18)
+    Q, pages = _bf16(rng, 4, 8, 128), torch.zeros(2, 2, 64, 128, dtype=torch.uint8, device=DEV)
+    O, lse = torch.full((4, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((4, 8), 7.0, device=DEV)
+    status = api.new_status(DEV)
+    api.pw_chunk_attn(Q, pages, pages, _i32([[0], [1]]), _i32([0, 0, 0]), _i32([3, 0]), max_q_len=max_q, O=O, lse=lse, status=status)
+    _ok(status)
+    assert bool((O == 7.0).all()) and bool((lse == 7.0).all())
+    none = api.pw_chunk_attn(Q[:0], pages, pages, _i32([[0]]), _i32([0, 0]), max_q_len=max_q, status=status)
+    _ok(status)
+    assert none.shape == (0, 8, 128)
+
+
+@pytest.mark.parametrize("qlens,max_q", [([1, 1, 1], 1), ([7], 7), ([180], 180)])
+def test_chunk_attn_special_queries_stay_in_their_row(qlens, max_q):
+    rng = np.random.default_rng(19)
+    ctx = [300] * len(qlens)
+    cu, cl, table, Q, Kp, Vp = _attn_inputs(rng, qlens, ctx, 8, 2)
+    T = int(cu[-1])
+    clean = ref.f64(Q)
+    Q[T // 2, 3, 77], Q[T - 1, 4, 0], Q[0, 5, 127] = float("nan"), float("inf"), -float("inf")
+    status = api.new_status(DEV)
+    lse = torch.empty(T, 8, device=DEV)
+    O = api.pw_chunk_attn(Q, torch.from_numpy(Kp).to(DEV), torch.from_numpy(Vp).to(DEV), _i32(table), _i32(cu), _i32(cl), max_q_len=max_q,
+                          k_scale=2.0 ** -6, v_scale=2.0 ** -6, lse=lse, status=status)
+    _ok(status)
+    bad = np.zeros((T, 8), bool)
+    bad[T // 2, 3] = bad[T - 1, 4] = bad[0, 5] = True
+    assert bool(O[torch.from_numpy(bad).to(DEV)].isnan().all()) and bool(lse[torch.from_numpy(bad).to(DEV)].isnan().all())
+    want, wl, bO, bl = ref.attn(clean, Kp, Vp, table, qlens, ctx, 2.0 ** -6, 2.0 ** -6, 128 ** -0.5)
+    good = torch.from_numpy(~bad).to(DEV)
+    ref.assert_bf16(O[good], want[~bad], bO[~bad])
+    assert (np.abs(ref.f64(lse[good]) - wl[~bad]) <= bl[~bad]).all()
+
+
+@pytest.mark.parametrize("cu,ctx", [([0, 3, 2], [1, 1]), ([0, 9, 4], [1, 1]), ([-1, 2, 4], [1, 1]), ([0, 2, 4], [-5, 1])])
+@pytest.mark.parametrize("max_q", [1, 200])
+def test_chunk_attn_bad_offsets_are_reported(cu, ctx, max_q):
+    """Falling offsets, offsets outside the rows, a negative context: recorded, and nothing outside the
+    buffers is touched (the guard rows stay)."""
+    rng = np.random.default_rng(25)
+    Q, pages = _bf16(rng, 4, 8, 128), torch.zeros(4, 2, 64, 128, dtype=torch.uint8, device=DEV)
+    guard = torch.full((6, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    status = api.new_status(DEV)
+    api.pw_chunk_attn(Q, pages, pages, _i32([[0, 1], [2, 3]]), _i32(cu), _i32(ctx), max_q_len=max_q, O=guard[1:5], status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == _lib.PW_ERR_INVALID_ARG
+    assert bool((guard[0] == 7.0).all()) and bool((guard[5] == 7.0).all())
+
+
 @pytest.mark.parametrize("qlens", [[1], [200]])
 @pytest.mark.parametrize("q_scale,sm", [(1e-20, 128 ** -0.5), (1e-3, 128 ** -0.5), (30.0, 128 ** -0.5), (1.0, 1e-6), (1e4, 1e-5)])
 def test_chunk_attn_score_ranges(qlens, q_scale, sm):
@@ -501,6 +562,30 @@ def test_captured_steps_replay_with_growing_contexts():
         want, _ = m.expected(qkv, [1] * B, c)
         _close(O, want, f"replay {step}")
         ctx += 1
+
+
+def test_two_captured_graphs_with_a_workspace_each():
+    """Two graphs, replayed at the same time on two streams."""
+    rng = np.random.default_rng(26)
+    jobs = []
+    for q, c in ((1, 3000), (150, 700)):
+        cu, cl, table, Q, Kp, Vp = _attn_inputs(rng, [q], [c], 8, 2)
+        args = (Q, torch.from_numpy(Kp).to(DEV), torch.from_numpy(Vp).to(DEV), _i32(table), _i32(cu), _i32(cl))
+        kw = dict(max_q_len=q, k_scale=2.0 ** -6, workspace=api.chunk_workspace(1, q, 8, 2, max_q_len=q, device=DEV))
+        want = api.pw_chunk_attn(*args, **kw)
+        torch.cuda.synchronize()
+        g, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+        with torch.cuda.graph(g):
+            api.pw_chunk_attn(*args, O=out, **kw)
+        jobs.append((g, out, want, torch.cuda.Stream(), args, kw))  # a graph keeps none of its tensors alive
+    for _ in range(5):
+        for g, out, _, s, _, _ in jobs:
+            with torch.cuda.stream(s):
+                out.zero_()
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _, _, _ in jobs:
+            assert torch.equal(out, want)
 
 
 def test_two_streams_with_a_workspace_each():
