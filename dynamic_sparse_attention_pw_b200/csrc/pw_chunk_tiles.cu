@@ -132,16 +132,19 @@ static __device__ __noinline__ void rescale(uint32_t o_addr, int no, uint32_t p_
 
 // Takes the NaN out of the values of the block at b0 (the pieces that thread t converts); the rows of the
 // tile that see such a key get one.  Rare, and so not inlined.
-static __device__ __noinline__ void take_nan(uint8_t *v, int t, int b0, const Shape shape, int ctx, int row, int rows, float *bad0, float *bad1)
+static __device__ __noinline__ void take_nan(uint8_t *v, int t, int b0, int lo, int hi, const Shape shape, int ctx, int row, int rows, float *bad0,
+                                             float *bad1)
 {
 #pragma unroll 1
     for (int q = t; q < kBlock * 8; q += 128) {
+        const int kp = b0 + (q >> 3);
+        if (kp < lo || kp >= hi)
+            continue; // any bytes
         uint4 *const at = reinterpret_cast<uint4 *>(v + q * 16);
         uint4 x = *at;
         if (!drop_nan(x))
             continue;
         *at = x;
-        const int kp = b0 + (q >> 3);
 #pragma unroll 1
         for (int r = 0; r < rows; ++r) {
             const int pos = shape.position(ctx, shape.token(row + r));
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Nor where one token of the tile sees a key and another does not: there NaN leaves the
                 // values and enters the sums of the rows that see it.
                 if (b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= j.hi - 1 - L.window))
-                    take_nan(sm.v[sv], t, b0, shape, j.ctx, j.row, j.rows, sm.bad[0][(nt[0] - 1) & 1u], sm.bad[1][(nt[1] - 1) & 1u]);
+                    take_nan(sm.v[sv], t, b0, j.lo, j.hi, shape, j.ctx, j.row, j.rows, sm.bad[0][(nt[0] - 1) & 1u], sm.bad[1][(nt[1] - 1) & 1u]);
 #pragma unroll 2
                 for (int i = 0; i < 8; ++i) {
                     const int q = t + 128 * i, key = q >> 3, c16 = q & 7;
