@@ -8,8 +8,9 @@
 // weights, rounded to f16, as three exact ones: four significant bits, the next four of what is left,
 // and the rest, at no more passes over V, since the parts lie side by side along N.  A weight of at
 // most 1 whose f16 bits are shifted right by 7 is the E4M3 code of 2^8 times the weight, cut off, with
-// the subnormal numbers of both formats in the same places, so a part is a shift and a subtraction
-// (conversions to and from E4M3 run at the rate of the exponential and took twice its time).
+// the subnormal numbers of both formats in the same places, so a part is a shift and a subtraction.
+// Four rows' codes of a key go out in one store: exponentials, parts and stores of a block took 461
+// cycles with conversions and a store a code, 260 so.
 //
 // The running maximum of a row is a reference that only has to keep its weights in range: it lies
 // above the scores and moves when one exceeds it, to 4 (base 2) above that score, so that a row's
@@ -27,6 +28,12 @@
 //   warp 8       load: page ids, TMA copies into the ring of K and V stages, job records
 //   warp 9       the products
 //   warp 10      the next tile's queries
+//
+// What bounds it: the bytes of the cache.  64 sequences of 500 to 16k tokens, 8 query heads a kv head
+// (1.1 GB): 191 to 205 us (B200s differ), 5.4 to 5.8 TB/s with launch and merge; four of 128k: 172 to
+// 181 us, 5.9 to 6.25 TB/s (a copy: 6.55).  With 20 rows (5 drafted tokens, 4 heads) the weights'
+// arithmetic takes longer than the bytes, 0.9 us a block of 128 keys against 0.75 us.  Small calls are
+// latency: 13.9 us for one token over 2k keys.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>

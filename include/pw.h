@@ -192,7 +192,7 @@ pw_status pw_group_noalloc(const int32_t *sel_pages, const int32_t *cu_seqlens,
  *   T           rows that the caller's buffers hold.  Rows from cu_seqlens[B] on (a padded
  *               batch) are neither read nor written.
  * The lengths are read on the device only, so a captured graph may be replayed after they
- * change.  Nothing here resets *dev_status: the first error is recorded and stays.
+ * change (between launches, not during one).  Nothing here resets *dev_status: the first error is recorded and stays.
  * Rows of heads: element (t, h, d) of a [T, H, 128] argument is at t * stride_t + h * stride_h + d.
  * Strides count elements and are multiples of 8; data starts on a 16-byte boundary.  An output's
  * rows must not overlap.
@@ -210,7 +210,8 @@ pw_status pw_group_noalloc(const int32_t *sel_pages, const int32_t *cu_seqlens,
  *                   NULL or rot_dim 0 = no rotation.  rot_dim is a multiple of 16, at most 128.
  *   Q_out, K_out    bf16 rows of heads; the same buffer and strides as the input, or no overlap
  *                   with any input
- * A position outside [0, max_pos) records PW_ERR_INVALID_ARG; its rows are not rotated. */
+ * A position outside [0, max_pos) records PW_ERR_INVALID_ARG; its rows are not rotated.
+ * Supported: Hq + Hk <= 131068. */
 pw_status pw_qk_norm_rope(const void *Q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
                           const void *K, int64_t k_stride_t, int64_t k_stride_h, int Hk,
                           const void *q_weight, int q_weight_stride, const void *k_weight,
@@ -228,7 +229,7 @@ pw_status pw_qk_norm_rope(const void *Q, int64_t q_stride_t, int64_t q_stride_h,
  * written.  Two tokens of one call must not share a slot.
  *   K, V              bf16 rows of heads, Hkv heads each
  *   K_pages, V_pages  uint8 [n_phys, Hkv, 64, 128], 16-byte aligned
- * Scales are positive and finite.  A position whose page lies outside the table's row, or whose
+ * Scales are positive and finite, 2 * Hkv <= 131068.  A position whose page lies outside the table's row, or whose
  * table entry is outside [0, n_phys), records PW_ERR_INVALID_ARG and is not written; so does a
  * position outside [0, max_pos) of the rotation's table. */
 pw_status pw_append(const void *K, int64_t k_stride_t, int64_t k_stride_h, const void *V,
@@ -253,8 +254,16 @@ pw_status pw_chunk_workspace_size(int B, int64_t T, int Hq, int Hkv, int max_q_l
  *   max_q_len       longest chunk of the batch, on the host.  It chooses the kernel; the results
  *                   are right for any positive value.
  *   workspace       pw_chunk_workspace_size bytes for the same B, T, Hq, Hkv and max_q_len; calls
- *                   that overlap in time must not share it.  It needs no clearing.
- * Supported: Hq % Hkv == 0, positions below 2^30.  sm_scale is positive and finite, scales too.
+ *                   that overlap in time must not share it (two captured graphs neither: a shared
+ *                   one makes wrong results, though no access outside the buffers).  It needs no
+ *                   clearing.
+ * What no token sees (behind a sequence's end, before its window, pages of nobody) may hold any
+ * bytes.  A NaN among the keys or values of a position makes NaN of every token that sees it (its
+ * whole row, or, of a value that the whole tile sees, that dimension), and of no other; an infinity
+ * or NaN in a query makes NaN of its own row.
+ * Results do not depend on timing: the same inputs give the same bits.
+ * Supported: Hq % Hkv == 0, positions below 2^30, T * Hq < 2^31 - 4096, n_phys * Hkv * 64 < 2^31.
+ * sm_scale is positive and finite, scales too.
  * A page-table entry outside [0, n_phys), or a position outside the table's row, records
  * PW_ERR_INVALID_ARG and nothing is read outside the cache. */
 pw_status pw_chunk_attn(const void *Q, int64_t q_stride_t, int64_t q_stride_h, int Hq,

@@ -92,7 +92,9 @@ def attn(Q, K_pages, V_pages, table, qlens, ctx, k_scale, v_scale, sm_scale, win
     Bounds before the output's rounding.  Scores: products of the tensor cores summed in fp32, off
     by at most 2^-20 of sum |q k|; that and the exponential (2^-21) move each weight by e relative,
     and the softmax by 2 e.  Weights enter P V rounded to f16 (half a step 2^-11; below 2^-14 an
-    absolute 2^-25 of a row whose largest weight is at least 1), summed in fp32."""
+    absolute 2^-25 of a row whose largest weight is at least 1; with few rows the largest is at least
+    2^-4, and the errors of its small weights, of either sign, stay inside the first term), summed in
+    fp32."""
     T, Hq, _ = Q.shape
     Hkv = K_pages.shape[1]
     G = Hq // Hkv
