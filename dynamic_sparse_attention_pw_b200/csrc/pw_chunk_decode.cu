@@ -55,15 +55,16 @@ constexpr int kQ = 2;
 constexpr float kAbove = 4.f;  // a row's reference moves to this much above its largest score (base 2)
 
 template <int NT> constexpr int kStagesFor = NT == 16 ? 3 : 2;
+template <int NT> constexpr int kCols = (3 * NT + 15) / 16 * 16; // columns of the weights: a whole number of cores
 
 template <int NT>
 struct __align__(1024) DecSmem {
     static constexpr int kStages = kStagesFor<NT>;
     uint8_t k[kStages][kBlock * 128]; // 128 keys x 128 dims
     uint8_t v[kStages][kBlock * 128];
-    // the weights as a matrix of 3 NT columns (part, row) by 128 keys, columns contiguous: cores of
-    // 8 keys by 16 columns (128 bytes), the cores of the same 8 keys side by side
-    uint8_t p[3 * NT * 128];
+    // the weights as a matrix of 3 NT columns (part, row; a few of padding behind) by 128 keys, columns
+    // contiguous: cores of 8 keys by 16 columns (128 bytes), the cores of the same 8 keys side by side
+    uint8_t p[kCols<NT> * 128];
     uint8_t q[kQ][2 * NT * 128];      // [tile % kQ][part, row][dim]
     float c[kQ][NT];                  // [tile % kQ]: factor of a row's scores
     int pos[kQ][NT];                  // [tile % kQ]: position of the row's token
@@ -152,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr uint32_t kTmemCols = NT == 16 ? 128 : 256;
     constexpr uint32_t kColO = 4 * NT; // two S, then the accumulator
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 2 * NT);
-    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, 3 * NT) | (1u << 15) | (1u << 16); // A (V^T) and B (P) MN-major
-    constexpr int kKeys8 = 3 * NT * 8; // bytes of P of 8 keys
+    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, kCols<NT>) | (1u << 15) | (1u << 16); // A (V^T) and B (P) MN-major
+    constexpr int kKeys8 = kCols<NT> * 8; // bytes of P of 8 keys
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 sm.nm[key] = key < rows ? -kNoMax : 0.f; // rows of padding score 0 and never move
             if (bar_or(bar, 128, !ok))
                 break;
-            const int R8 = (rows + 7) >> 3;                                 // groups of eight rows
+            const int R8 = max(rows - static_cast<int>(h4) + 7, 0) >> 3;    // this half's groups of four rows
             const int pos_lo = sm.pos[qb][0], pos_hi = sm.pos[qb][rows - 1]; // first and last token
             const float *const fac = sm.c[qb] + h4;
             F2 l[NT / 8][2];
@@ -243,17 +244,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (i0 < R8) {
                         uint32_t a[2][4], b[2][4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < 2 && i0 + i < NT / 8; ++i) {
                             tmem_ld4(s_addr + 8 * (i0 + i), a[i]);
                             tmem_ld4(s_addr + NT + 8 * (i0 + i), b[i]);
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < 2 && i0 + i < NT / 8; ++i) {
                             tmem_wait(a[i]);
                             tmem_wait(b[i]);
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < 2 && i0 + i < NT / 8; ++i) {
                             const float4 f = *reinterpret_cast<const float4 *>(fac + 8 * (i0 + i));
                             y[i0 + i][0] = mul2(add2(pack2(__uint_as_float(a[i][0]), __uint_as_float(a[i][1])),
                                                      pack2(__uint_as_float(b[i][0]), __uint_as_float(b[i][1]))), pack2(f.x, f.y));
@@ -675,11 +676,11 @@ cudaError_t launch(ChunkLaunch &L, int sms, cudaStream_t st)
 
 } // namespace
 
-size_t decode_workspace(int rows) { return rows <= 16 ? workspace_bytes<16>() : workspace_bytes<32>(); }
+size_t decode_workspace(int rows) { return rows <= 16 ? workspace_bytes<16>() : rows <= 24 ? workspace_bytes<24>() : workspace_bytes<32>(); }
 
 cudaError_t decode_launch(ChunkLaunch &L, int rows, int sms, cudaStream_t st)
 {
-    return rows <= 16 ? launch<16>(L, sms, st) : launch<32>(L, sms, st);
+    return rows <= 16 ? launch<16>(L, sms, st) : rows <= 24 ? launch<24>(L, sms, st) : launch<32>(L, sms, st);
 }
 
 } // namespace chunk

@@ -252,6 +252,10 @@ ATTN_CASES = [
     ([1, 0, 1, 0], [300, 20, 128, 0], 12, 4, 0, None),
     ([5, 2, 8], [700, 0, 131], 8, 2, 0, None),
     ([3], [2000], 64, 2, 0, None),         # 32 heads a group
+    ([6, 1, 5, 0], [900, 0, 127, 3], 8, 2, 0, None),  # 24 rows a tile
+    ([3, 2], [4000, 64], 14, 2, 200, None),           # 21
+    ([1], [700], 17, 1, 0, None),
+    ([1, 1], [2500, 1], 50, 2, 0, None),              # 25
     ([2], [500], 33, 1, 0, None),          # an odd number of heads a group
     ([1], [500], 130, 1, 0, None),
     ([16], [0], 8, 1, 0, None),
