@@ -217,21 +217,16 @@ struct Pieces {
     __device__ __forceinline__ void begin(const ChunkLaunch &L, const Shape &p, int cta, int lane)
     {
         const int B = L.tb.B, grid = gridDim.x;
-        // All blocks.  Four sequences a lane at once, so that their loads overlap; the first 128 counts stay.
-        int64_t mine[4] = {0, 0, 0, 0}, total = 0;
-        for (int base = 0; base < B; base += 128) {
-            Sequence q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                q[e] = base + 32 * e + lane < B ? sequence(L, base + 32 * e + lane) : Sequence{0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (base + 32 * e < B) {
-                    const int64_t n = head_blocks<NT>(p, q[e].qlen, q[e].ctx, lane);
-                    total += n;
-                    if (base == 0)
-                        mine[e] = n;
-                }
+        // All blocks, 32 sequences at a time; the first 32 counts stay.  (Four groups of loads at once hid
+        // their latency in large batches, but the code of it cost a small call more.)
+        int64_t mine = 0, total = 0;
+#pragma unroll 1
+        for (int base = 0; base < B; base += 32) {
+            const Sequence q = base + lane < B ? sequence(L, base + lane) : Sequence{0, 0, 0};
+            const int64_t n = head_blocks<NT>(p, q.qlen, q.ctx, lane);
+            total += n;
+            if (base == 0)
+                mine = n;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
@@ -251,8 +246,8 @@ struct Pieces {
         int64_t rest = x, per_head = 1;
         b = -1;
         for (int base = 0; b < 0 && base < B; base += 32) {
-            int64_t n = base == 0 ? mine[0] : base == 32 ? mine[1] : base == 64 ? mine[2] : mine[3];
-            if (base >= 128) {
+            int64_t n = mine;
+            if (base > 0) {
                 const Sequence q = base + lane < B ? sequence(L, base + lane) : Sequence{0, 0, 0};
                 n = head_blocks<NT>(p, q.qlen, q.ctx, lane);
             }

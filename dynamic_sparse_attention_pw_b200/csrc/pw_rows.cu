@@ -14,8 +14,9 @@
 // instructions, 71% of the issue slots at 67% of the memory rate.)  How many heads a warp takes is a
 // matter of filling the GPU: few tokens, one group of four heads each; many, up to kMost groups.
 // A prompt of 16k tokens, 64 + 8 heads (0.6 GB): 108 us, 5.65 TB/s; sixteen groups a warp 113 us where two
-// took 180 us.  Append of two such prompts (8 + 8 heads, 0.2 GB): 55 us; its warps have only four groups,
-// and the chain position, page, table row before the first store bounds them.
+// took 180 us.  Append of two such prompts (8 + 8 heads, 0.2 GB): 50 us, 55 from a cold cache (61 with the
+// keys' factors formed before the values went out); its warps have only four groups, and the chain
+// position, page, table row before the first store bounds them.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -359,14 +360,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_append(const AppendLaunch L, in
         set_status(L.status, PW_ERR_INVALID_ARG);
         return;
     }
-    Turn<kInter> turn;
-    turn.form(L.rope, ck, l, pos, L.k.w_stride == 0 ? L.k.w : nullptr, L.inv_k);
     const size_t row = (static_cast<size_t>(phys) * Hkv * kPageTokens + (pos & 63)) * kHeadDim;
     values.run(L.v, h0, Times{pack2(L.inv_v, L.inv_v)}, 0.f, [&](int h, const F2 (&x)[8]) {
         uint2 *p = reinterpret_cast<uint2 *>(L.V + row + static_cast<size_t>(h) * (kPageTokens * kHeadDim));
         const uint2 a = codes8(x), c = codes8(x + 4); // neighbouring chunks
         *reinterpret_cast<uint4 *>(p + cv.c0) = make_uint4(a.x, a.y, c.x, c.y);
     });
+    Turn<kInter> turn; // behind the values, which need no table row
+    turn.form(L.rope, ck, l, pos, L.k.w_stride == 0 ? L.k.w : nullptr, L.inv_k);
     keys.run(L.k, h0, turn, L.eps, [&](int h, const F2 (&x)[8]) {
         uint2 *p = reinterpret_cast<uint2 *>(L.K + row + static_cast<size_t>(h) * (kPageTokens * kHeadDim));
         p[ck.c0] = codes8(x);
