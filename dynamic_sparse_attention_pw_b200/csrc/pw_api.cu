@@ -64,7 +64,7 @@ size_t workspace_for(const Sizes &z, int Hkv)
 
 extern "C" {
 
-int pw_version(void) { return 101; }
+int pw_version(void) { return 102; }
 
 const char *pw_status_string(int s)
 {

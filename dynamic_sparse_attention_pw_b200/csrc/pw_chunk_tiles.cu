@@ -49,7 +49,9 @@ struct __align__(1024) TileSmem {
     uint8_t v[kNV][kBlock * 128];   // E4M3 as stored
     uint8_t v16[2][2][kBlock * 128]; // [block % 2][dims 0-63, 64-127][key][dim] f16, swizzled
     float c[2][2][kHalf];           // [half][its tile % 2]: factor of a row's scores
-    float bad[2][2][kHalf];         // [half][its tile % 2]: NaN for a row that sees a value taken out as NaN, else 0
+    // [half][its tile % 3]: NaN for a row that sees a value taken out as NaN, else 0.  Three, because a
+    // tile's are read at its end, when the queries of the tile after the next may be on their way.
+    float bad[2][3][kHalf];
     Job job[kJobs];
     uint64_t job_full[kJobs], job_empty[kJobs];
     uint64_t q_full[2], q_empty[2];
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
             float l0, l1;
             unpack2(add2(l[0], l[1]), l0, l1);
-            const float sum = (l0 + l1) + sm.bad[a][nt & 1u][r & 127], inv = L.v_scale / sum;
+            const float sum = (l0 + l1) + sm.bad[a][nt % 3u][r & 127], inv = L.v_scale / sum;
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t o[32];
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4 *>(sm.q[a][1] + at) = make_uint4(a2.x, a2.y, b2.x, b2.y);
                 }
                 sm.c[a][nt[a] & 1u][t] = q_factor(e, L.score_scale);
-                sm.bad[a][nt[a] & 1u][t] = 0.f;
+                sm.bad[a][nt[a] % 3u][t] = 0.f;
                 fence_proxy_async_smem();
                 warp_arrive(&sm.q_full[a], lane);
                 ++nt[a];
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Nor where one token of the tile sees a key and another does not: there NaN leaves the
                 // values and enters the sums of the rows that see it.
                 if (b0 + kBlock - 1 > pos_lo || (L.window > 0 && b0 <= j.hi - 1 - L.window))
-                    take_nan(sm.v[sv], t, b0, j.lo, j.hi, shape, j.ctx, j.row, j.rows, sm.bad[0][(nt[0] - 1) & 1u], sm.bad[1][(nt[1] - 1) & 1u]);
+                    take_nan(sm.v[sv], t, b0, j.lo, j.hi, shape, j.ctx, j.row, j.rows, sm.bad[0][(nt[0] + 2u) % 3u], sm.bad[1][(nt[1] + 2u) % 3u]);
 #pragma unroll 2
                 for (int i = 0; i < 8; ++i) {
                     const int q = t + 128 * i, key = q >> 3, c16 = q & 7;

@@ -190,7 +190,7 @@ pw_status pw_group_noalloc(const int32_t *sel_pages, const int32_t *cu_seqlens,
  *   ctx_lens    int32 [B]    tokens of each sequence that are in the cache already; NULL = 0.
  *                            Token i of sequence b has position ctx_lens[b] + i.
  *   T           rows that the caller's buffers hold.  Rows from cu_seqlens[B] on (a padded
- *               batch) are neither read nor written.
+ *               batch) have no effect, and outputs keep what they hold there.
  * The lengths are read on the device only, so a captured graph may be replayed after they
  * change (between launches, not during one).  Nothing here resets *dev_status: the first error is recorded and stays.
  * Rows of heads: element (t, h, d) of a [T, H, 128] argument is at t * stride_t + h * stride_h + d.
