@@ -92,6 +92,8 @@ def binding():
     if _binding is None:
         load()
         try:
+            import torch  # noqa: F401 - the libraries that the module is linked against
+
             from . import _pw_binding
         except ImportError as e:
             raise RuntimeError("_pw_binding.so is missing or does not load; build it with "

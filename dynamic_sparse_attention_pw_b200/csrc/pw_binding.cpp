@@ -222,8 +222,11 @@ struct OnDevice {
     }
     ~OnDevice()
     {
-        if (before >= 0)
-            c10::cuda::set_device(before);
+        try {
+            if (before >= 0)
+                c10::cuda::set_device(before);
+        } catch (...) { // the next call on that device says why
+        }
     }
 };
 

@@ -463,6 +463,46 @@ def test_chunk_attn_same_bits_every_time_and_any_batch_order():
         assert all(torch.equal(runs[0], r) for r in runs[1:])
 
 
+@pytest.mark.parametrize("change", [
+    dict(Q=lambda a: a["Q"].half()), dict(Q=lambda a: a["Q"][..., :64]), dict(Q=lambda a: a["Q"].transpose(1, 2)),
+    dict(K_pages=lambda a: a["K_pages"][:1]), dict(K_pages=lambda a: a["K_pages"].cpu()), dict(V_pages=lambda a: a["V_pages"].view(torch.int8)),
+    dict(page_table=lambda a: a["page_table"].long()), dict(page_table=lambda a: a["page_table"][:1]),
+    dict(cu_seqlens=lambda a: a["cu_seqlens"].long()), dict(ctx_lens=lambda a: a["ctx_lens"][:1]),
+    dict(lse=lambda a: torch.empty(4, 7, device=DEV)), dict(O=lambda a: a["Q"][:, :4].clone()), dict(O=lambda a: a["Q"].float()),
+    dict(workspace=lambda a: torch.empty(1 << 20, dtype=torch.uint8)), dict(status=lambda a: torch.zeros(1, device=DEV)),
+])
+def test_chunk_attn_refuses_tensors_that_do_not_fit(change):
+    rng = np.random.default_rng(27)
+    a = dict(Q=_bf16(rng, 4, 8, 128), K_pages=torch.zeros(2, 2, 64, 128, dtype=torch.uint8, device=DEV),
+             V_pages=torch.zeros(2, 2, 64, 128, dtype=torch.uint8, device=DEV), page_table=_i32([[0], [1]]),
+             cu_seqlens=_i32([0, 1, 4]), ctx_lens=_i32([0, 5]), max_q_len=3)
+    api.pw_chunk_attn(**a)
+    with pytest.raises(AssertionError):
+        api.pw_chunk_attn(**{**a, **{k: f(a) for k, f in change.items()}})
+    torch.cuda.synchronize()
+
+
+def test_calls_refuse_sizes_on_the_host():
+    rng = np.random.default_rng(28)
+    Q, pages, cu = _bf16(rng, 2, 7, 128), torch.zeros(2, 2, 64, 128, dtype=torch.uint8, device=DEV), _i32([0, 2])
+    with pytest.raises(_lib.PwError):  # 7 query heads over 2
+        api.pw_chunk_attn(Q, pages, pages, _i32([[0]]), cu, max_q_len=2)
+    with pytest.raises(_lib.PwError):
+        api.pw_chunk_attn(Q[:, :6], pages, pages, _i32([[0]]), cu, max_q_len=2, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(_lib.PwError):
+        api.pw_qk_norm_rope(Q, None, cu, rope=torch.zeros(8, 24, device=DEV))
+    with pytest.raises(_lib.PwError):
+        api.pw_append(Q[:, :2], Q[:, :2], pages, pages, _i32([[0]]), cu, k_scale=0.0)
+    with pytest.raises(AssertionError):
+        api.pw_append(Q[:, :3], Q[:, :2], pages, pages, _i32([[0]]), cu)
+    with pytest.raises(AssertionError):
+        api.pw_qk_norm_rope(Q, None, cu, q_weight=_bf16(rng, 6, 128))
+    with pytest.raises(AssertionError):
+        api.pw_qk_norm_rope(Q, None, cu, Q_out=_bf16(rng, 2, 6, 128))
+    torch.cuda.synchronize()
+    assert bool((pages == 0).all())
+
+
 # ---------------------------------------------------------------------------------------
 # Together, as they are used
 # ---------------------------------------------------------------------------------------
