@@ -19,8 +19,8 @@
 //   warp 13      the products
 // What bounds it: the chain of a half's block -- softmax 1650 to 2050 cycles, wake-up 350, P V 570, S 600,
 // S back to the softmax 240 -- of which the other half's hides most: a block of 256 rows takes 3500
-// cycles, the tensor cores' share of it 2400.  2048 tokens at 32k (2.13 TFLOP): 1.66 ms from a cold cache,
-// 1.95 ms in a row under the power limit.  Tried and slower: a product warp for each half (the halves
+// cycles, the tensor cores' share of it 2400.  2048 tokens at 32k (2.13 TFLOP): 1.63 ms from a cold cache,
+// 1.88 ms in a row under the power limit.  Tried and slower: a product warp for each half (the halves
 // fall into step: 2.14 ms against 1.73), steps of 64 keys with S a step ahead (M = 128, N = 64 products
 // take as long as N = 128: 2.48), two threads a row (1.79), part of the exponentials on the
 // multiply-add units (a quarter of them 1.86), waits that spin (1.79).
