@@ -49,8 +49,10 @@ struct __align__(1024) TileSmem {
     uint8_t v[kNV][kBlock * 128];   // E4M3 as stored
     uint8_t v16[2][2][kBlock * 128]; // [block % 2][dims 0-63, 64-127][key][dim] f16, swizzled
     float c[2][2][kHalf];           // [half][its tile % 2]: factor of a row's scores
-    // [half][its tile % 3]: NaN for a row that sees a value taken out as NaN, else 0.  Three, because a
-    // tile's are read at its end, when the queries of the tile after the next may be on their way.
+    // [half][its tile % 3]: NaN for a row that sees a value taken out as NaN, else 0.  Any of the V warps
+    // marks any row, without waiting for the others, so the thread that reads a mark clears it.  Three,
+    // because a tile's are read at its end, when the values of the next two tiles may be marked already; those
+    // of the third come behind products that its softmax warps let go after that end.
     float bad[2][3][kHalf];
     Job job[kJobs];
     uint64_t job_full[kJobs], job_empty[kJobs];
@@ -173,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     TileSmem &sm = *reinterpret_cast<TileSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
 
+    for (int i = tid; i < 2 * 3 * kHalf; i += kThreads)
+        (&sm.bad[0][0][0])[i] = 0.f;
     if (tid == 0) {
         for (int i = 0; i < kJobs; ++i) {
             mbar_init(&sm.job_full[i], 1);
@@ -319,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t at = (static_cast<int64_t>(j.tok0) + tok) * L.Hq + j.h * L.G + flat - tok * L.G;
             float l0, l1;
             unpack2(add2(l[0], l[1]), l0, l1);
-            const float sum = (l0 + l1) + sm.bad[a][nt % 3u][r & 127], inv = L.v_scale / sum;
+            float *const mark = &sm.bad[a][nt % 3u][r & 127];
+            const float sum = (l0 + l1) + *mark, inv = L.v_scale / sum;
+            *mark = 0.f;
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t o[32];
@@ -397,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4 *>(sm.q[a][1] + at) = make_uint4(a2.x, a2.y, b2.x, b2.y);
                 }
                 sm.c[a][nt[a] & 1u][t] = q_factor(e, L.score_scale);
-                sm.bad[a][nt[a] % 3u][t] = 0.f;
                 fence_proxy_async_smem();
                 warp_arrive(&sm.q_full[a], lane);
                 ++nt[a];

@@ -1,0 +1,82 @@
+"""pw_chunk_attn where the values are what can go wrong: NaN marks of short tiles, and equal bits of
+repeated calls on ragged batches (tokens_ref.py holds the plain 64-bit forms)."""
+import numpy as np
+import pytest
+import torch
+
+from dynamic_sparse_attention_pw_b200 import api
+
+import tokens_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+S = 2.0 ** -6  # cache scale
+
+
+def _i32(x):
+    return torch.from_numpy(np.ascontiguousarray(x, np.int32)).to(DEV)
+
+
+def _codes(rng, shape):
+    x = torch.from_numpy(np.clip(rng.standard_normal(shape) * 64.0, -448, 448))
+    return x.to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+
+
+def _dev(x):
+    return torch.from_numpy(x).to(DEV)
+
+
+@pytest.mark.parametrize("B,q,ctx,Hq,Hkv,max_q", [
+    (500, 16, 0, 8, 1, 16),     # one half of a large tile, one block
+    (500, 16, 120, 8, 1, 16),   # two blocks
+    (300, 30, 0, 8, 1, 30),     # both halves
+    (700, 4, 0, 8, 1, 4),       # the small tiles
+])
+def test_nan_marks_of_many_short_tiles(B, q, ctx, Hq, Hkv, max_q):
+    """Every CTA works on many short tiles whose first block holds NaN values that some rows see: those
+    rows are NaN and no other, in every one of several calls."""
+    rng = np.random.default_rng(1)
+    qlens, ctxs = [q] * B, [ctx] * B
+    cu, cl = ref.batch(qlens, ctxs)
+    table, n_phys = ref.pages_for(qlens, ctxs, rng)
+    Kp, Vp = _codes(rng, (n_phys, Hkv, 64, 128)), _codes(rng, (n_phys, Hkv, 64, 128))
+    first = rng.integers(1, q, B)  # first token of each sequence that sees a NaN
+    first[::5] = q                 # none does
+    for b in range(B):
+        if first[b] < q:
+            p = ctx + first[b]
+            Vp[table[b, p // 64], :, p % 64, rng.integers(0, 128)] = 0x7F
+    # rows far apart, so that the queries of a tile arrive at different times
+    Q = torch.from_numpy(rng.standard_normal((cu[-1], 16 * Hq, 128), np.float32)).to(torch.bfloat16).to(DEV)[:, ::16]
+    sees = torch.from_numpy((np.arange(q)[None] >= first[:, None]).reshape(-1)).to(DEV)
+    args = (Q, _dev(Kp), _dev(Vp), _i32(table), _i32(cu), _i32(cl))
+    clean = _dev(np.where((Vp & 0x7F) == 0x7F, 0, Vp).astype(np.uint8))
+    kw = dict(max_q_len=max_q, k_scale=S, v_scale=S, workspace=api.chunk_workspace(B, int(cu[-1]), Hq, Hkv, max_q_len=max_q, device=DEV))
+    want = api.pw_chunk_attn(args[0], args[1], clean, *args[3:], **kw)
+    for i in range(10):
+        got = api.pw_chunk_attn(*args, **kw)
+        torch.cuda.synchronize()
+        assert bool(got[sees].isnan().any(-1).all()), i
+        assert torch.equal(got[~sees], want[~sees]), i
+
+
+@pytest.mark.parametrize("qlens,ctx,Hq,Hkv,window", [
+    ([1] * 9, [40 * 5 ** (i % 6) for i in range(9)], 16, 2, 0),       # tiles of 16 rows
+    ([5, 1, 4, 0, 5], [3000, 9000, 64, 10, 700], 8, 2, 0),             # 24
+    ([7, 8, 1], [5000, 100, 20000], 8, 2, 0),                          # 32
+    ([200, 1, 0, 333, 70], [4000, 9000, 5, 0, 1500], 8, 2, 0),         # large ones
+    ([200, 1, 0, 333, 70], [4000, 9000, 5, 0, 1500], 8, 2, 600),
+])
+def test_ragged_batches_give_the_same_bits_again(qlens, ctx, Hq, Hkv, window):
+    rng = np.random.default_rng(2)
+    cu, cl = ref.batch(qlens, ctx)
+    table, n_phys = ref.pages_for(qlens, ctx, rng)
+    Q = torch.from_numpy(rng.standard_normal((cu[-1], Hq, 128))).to(torch.bfloat16).to(DEV)
+    args = (Q, _dev(_codes(rng, (n_phys, Hkv, 64, 128))), _dev(_codes(rng, (n_phys, Hkv, 64, 128))), _i32(table), _i32(cu), _i32(cl))
+    runs = []
+    for _ in range(8):
+        lse = torch.empty(Q.shape[:2], device=DEV)
+        runs.append((api.pw_chunk_attn(*args, max_q_len=max(qlens), k_scale=S, v_scale=S, window=window, lse=lse), lse))
+    torch.cuda.synchronize()
+    for O, lse in runs[1:]:
+        assert torch.equal(O, runs[0][0]) and torch.equal(lse, runs[0][1])
