@@ -61,6 +61,13 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b)
     return d;
 }
 
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // What the tiles of a call depend on besides their sequence.
 struct Shape {
     int G, window, last; // last position a page table's row can hold
@@ -398,8 +405,15 @@ __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n)
 
 // ---------------------------------------------------------------------------------------
 // Queries: a row times the power of two that brings its largest magnitude into [128, 256), split
-// into two E4M3 parts whose sum is exact for every element within 2^9 of the largest (a bf16 value
-// has 8 significant bits, a part 4).
+// into two 8-bit parts.  The first is the nearest E4M3 value.  Of the 8 significant bits of a bf16 value
+// that leaves 3 (the rest is at most half a step), so that the second needs range rather than bits:
+//   Rest::kE5M2     the rest as E5M2 (3 bits, steps down to 2^-16), where both parts are summed in
+//                   one accumulator: their products differ in the instruction's operand type alone;
+//   Rest::kE4M3Up5  2^5 times the rest as E4M3 (4 bits, steps down to 2^-9), where the parts have accumulators
+//                   of their own and a factor costs nothing.
+// Either sum is exact for every element within 2^13 of the row's largest (the first part keeps its four bits
+// down to 2^-6); below, it is off by at most 2^-14 (2^-15), 2^-21 (2^-22) of the largest.  With the rest as plain
+// E4M3, whose steps end at 2^-9, an element 2^13 below the largest was off by up to 2^-4 of itself.
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t max_exp8(const uint4 v)
 {
@@ -423,6 +437,18 @@ __device__ __forceinline__ void e4m3x2_to_f32(uint32_t pair, float &lo, float &h
     hi = __high2float(h);
 }
 
+enum class Rest { kE5M2, kE4M3Up5 };
+constexpr float kRestUp = 32.f; // kE4M3Up5
+
+// Two f32 -> packed E5M2 pair (round to nearest even); `lo` lands in the low byte.
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi)
+{
+    uint16_t d;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+template <Rest kRest>
 __device__ __forceinline__ void split_q8(const uint4 v, float scale, uint2 &q1, uint2 &q2)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -433,7 +459,7 @@ __device__ __forceinline__ void split_q8(const uint4 v, float scale, uint2 &q1, 
         a[i] = e4m3x2(x0, x1);
         float y0, y1;
         e4m3x2_to_f32(a[i], y0, y1);
-        b[i] = e4m3x2(x0 - y0, x1 - y1);
+        b[i] = kRest == Rest::kE5M2 ? e5m2x2(x0 - y0, x1 - y1) : e4m3x2((x0 - y0) * kRestUp, (x1 - y1) * kRestUp);
     }
     q1 = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16));
     q2 = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
@@ -447,7 +473,7 @@ __device__ __forceinline__ float q_factor(uint32_t e, float score_scale)
     return e == 255u ? __int_as_float(0x7FC00000) : fmaxf(score_scale * exp2i(-q_exp(e)), 1e-30f);
 }
 
-// Sixteen lanes of a half-warp (l = lane % 16) bring one row: its two parts into rows r1 and r2 of a
+// Sixteen lanes of a half-warp (l = lane % 16) bring one row: its two parts (kE4M3Up5) into rows r1 and r2 of a
 // K-major operand tile (128-byte rows, 128-byte swizzle).  Returns the row's factor.
 // v: the lane's eight elements.
 __device__ __forceinline__ float stage_q_row(const uint4 v, uint8_t *tile, int r1, int r2, int l, float score_scale)
@@ -458,7 +484,7 @@ __device__ __forceinline__ float stage_q_row(const uint4 v, uint8_t *tile, int r
         e = max(e, __shfl_xor_sync(kFull, e, d));
     const int s = q_exp(e);
     uint2 q1, q2;
-    split_q8(v, exp2i(s), q1, q2);
+    split_q8<Rest::kE4M3Up5>(v, exp2i(s), q1, q2);
     const int in = (l & 1) * 8;
     *reinterpret_cast<uint2 *>(tile + attn::swz(r1, l >> 1) + in) = q1;
     *reinterpret_cast<uint2 *>(tile + attn::swz(r2, l >> 1) + in) = q2;

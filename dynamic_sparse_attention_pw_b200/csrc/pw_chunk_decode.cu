@@ -4,7 +4,7 @@
 // is unpacked: a block of 128 keys is the M = 128 operand of
 //   S^T = K [q1 q2]        (M = keys, N = 2 NT, K = 128 dims; E4M3)
 //   O^T += V^T [P1 P2 P3]  (M = dims, N = 3 NT, K = 128 keys; E4M3, V read as stored, MN-major)
-// straight from the bytes that TMA landed.  Queries enter as two exact E4M3 parts (pw_chunk.cuh),
+// straight from the bytes that TMA landed.  Queries enter as two E4M3 parts, q2 times 2^5 (pw_chunk.cuh),
 // weights, rounded to f16, as three exact ones: four significant bits, the next four of what is left,
 // and the rest, at no more passes over V, since the parts lie side by side along N.  A weight of at
 // most 1 whose f16 bits are shifted right by 7 is the E4M3 code of 2^8 times the weight, cut off, with
@@ -257,10 +257,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int i = 0; i < 2 && i0 + i < NT / 8; ++i) {
                             const float4 f = *reinterpret_cast<const float4 *>(fac + 8 * (i0 + i));
-                            y[i0 + i][0] = mul2(add2(pack2(__uint_as_float(a[i][0]), __uint_as_float(a[i][1])),
-                                                     pack2(__uint_as_float(b[i][0]), __uint_as_float(b[i][1]))), pack2(f.x, f.y));
-                            y[i0 + i][1] = mul2(add2(pack2(__uint_as_float(a[i][2]), __uint_as_float(a[i][3])),
-                                                     pack2(__uint_as_float(b[i][2]), __uint_as_float(b[i][3]))), pack2(f.z, f.w));
+                            const F2 down = pack2(1.f / kRestUp, 1.f / kRestUp);
+                            y[i0 + i][0] = mul2(fma2(pack2(__uint_as_float(b[i][0]), __uint_as_float(b[i][1])), down,
+                                                     pack2(__uint_as_float(a[i][0]), __uint_as_float(a[i][1]))), pack2(f.x, f.y));
+                            y[i0 + i][1] = mul2(fma2(pack2(__uint_as_float(b[i][2]), __uint_as_float(b[i][3])), down,
+                                                     pack2(__uint_as_float(a[i][2]), __uint_as_float(a[i][3]))), pack2(f.z, f.w));
                         }
                     }
                 tc_fence_before();

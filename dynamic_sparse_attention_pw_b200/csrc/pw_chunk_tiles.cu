@@ -1,9 +1,9 @@
 // pw_chunk_tiles.cu -- pw_chunk_attn for many rows: chunks of a prompt.
 //
 // A tile is 256 rows, two halves of 128, against blocks of 128 keys.  Per half and block
-//   S = q1 K^T + q2 K^T   (M = 128 rows, N = 128 keys; E4M3: K as stored, the query's exact parts)
+//   S = q1 K^T + q2 K^T   (M = 128 rows, N = 128 keys; E4M3 K as stored, the query's E4M3 and E5M2 parts)
 //   O += P V              (M = 128 rows, N = 128 dims, K = 128 keys; f16: P from TMEM, V converted)
-// The E4M3 products of the two query parts take as long as one bf16 product would and spare the
+// The 8-bit products of the two query parts take as long as one bf16 product would and spare the
 // conversion of K; V is converted (exactly) to f16 once for both halves.  The halves alternate: while
 // one is in the softmax, the tensor cores work for the other.  The softmax is one thread a row: no
 // reduction crosses threads.
@@ -44,7 +44,7 @@ constexpr int kNK = 3, kNV = 2; // K and V stages
 constexpr float kRaise = 15.f;  // a row's reference moves when a score exceeds it by more (base 2); f16 ends at 2^16
 
 struct __align__(1024) TileSmem {
-    uint8_t q[2][2][kHalf * 128];   // [half][part][row][dim] E4M3
+    uint8_t q[2][2][kHalf * 128];   // [half][part][row][dim] E4M3, E5M2
     uint8_t k[kNK][kBlock * 128];   // E4M3, swizzled by the copy
     uint8_t v[kNV][kBlock * 128];   // E4M3 as stored
     uint8_t v16[2][2][kBlock * 128]; // [block % 2][dims 0-63, 64-127][key][dim] f16, swizzled
@@ -74,13 +74,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
                  "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
                  : "memory");
-}
-
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 
 __device__ __forceinline__ int halves(const Job &j) { return j.rows > kHalf ? 2 : 1; }
@@ -168,7 +161,7 @@ static __device__ __noinline__ void take_nan(uint8_t *v, int t, int b0, int lo, 
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_tiles(const ChunkLaunch L, const __grid_constant__ CUtensorMap map_k)
 {
-    constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 128);
+    constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 128), kIdescRest = kIdescS | (1u << 7); // A: E5M2
     constexpr uint32_t kIdescO = idesc_f16_f32(128, 128, false, true);
     constexpr uint32_t kColS = 128, kColO = 256; // S / P of the halves at columns 0 and 128, O at 256 and 384
     extern __shared__ uint8_t smem_raw[];
@@ -396,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint2 a1, a2, b1, b2;
-                    split_q8(v[2 * i], up, a1, a2);
-                    split_q8(v[2 * i + 1], up, b1, b2);
+                    split_q8<Rest::kE5M2>(v[2 * i], up, a1, a2);
+                    split_q8<Rest::kE5M2>(v[2 * i + 1], up, b1, b2);
                     const uint32_t at = attn::swz(t, i);
                     *reinterpret_cast<uint4 *>(sm.q[a][0] + at) = make_uint4(a1.x, a1.y, b1.x, b1.y);
                     *reinterpret_cast<uint4 *>(sm.q[a][1] + at) = make_uint4(a2.x, a2.y, b2.x, b2.y);
@@ -588,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) // four steps of each query part
                                 mma_f8_ss(tmem + a * kColS, dq + ((a * 2 * kHalf * 128 + (kk >> 2) * kHalf * 128 + (kk & 3) * 32) >> 4),
-                                          dk + ((sk * kBlock * 128 + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
+                                          dk + ((sk * kBlock * 128 + (kk & 3) * 32) >> 4), kk < 4 ? kIdescS : kIdescRest, kk > 0);
                             mma_commit(&sm.s_full[a]);
                             if (k == nblk - 1)
                                 mma_commit(&sm.q_empty[a]);

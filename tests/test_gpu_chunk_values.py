@@ -1,5 +1,5 @@
-"""pw_chunk_attn where the values are what can go wrong: NaN marks of short tiles, and equal bits of
-repeated calls on ragged batches (tokens_ref.py holds the plain 64-bit forms)."""
+"""pw_chunk_attn where the values are what can go wrong: NaN marks of short tiles, equal bits of repeated
+calls on ragged batches, queries with one large element (tokens_ref.py holds the plain 64-bit forms)."""
 import numpy as np
 import pytest
 import torch
@@ -80,3 +80,32 @@ def test_ragged_batches_give_the_same_bits_again(qlens, ctx, Hq, Hkv, window):
     torch.cuda.synchronize()
     for O, lse in runs[1:]:
         assert torch.equal(O, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
+@pytest.mark.parametrize("qlens,ctx", [([1], [700]), ([5, 2], [300, 64]), ([8], [300]), ([150, 40], [200, 0])])
+@pytest.mark.parametrize("octaves", [10, 12, 13, 14, 18])
+def test_queries_with_one_large_element(qlens, ctx, octaves):
+    """One element of every query lies octaves above the others, in a dimension in which the keys are next to
+    nothing: the scores are what the small elements make of them.  Elements within 2^13 of the largest enter
+    exactly, smaller ones are off by at most 2^-21 of the largest."""
+    rng = np.random.default_rng(octaves)
+    Hq, Hkv, big = 8, 2, 37
+    cu, cl = ref.batch(qlens, ctx)
+    table, n_phys = ref.pages_for(qlens, ctx, rng)
+    Kp, Vp = _codes(rng, (n_phys, Hkv, 64, 128)), _codes(rng, (n_phys, Hkv, 64, 128))
+    Kp[..., big] = rng.integers(0, 2, Kp.shape[:-1])  # zero, or the smallest code
+    q = rng.uniform(1.0, 2.0, (cu[-1], Hq, 128)) * rng.choice([-1.0, 1.0], (cu[-1], Hq, 128))
+    q[..., big] = 2.0 ** octaves
+    Q = torch.from_numpy(q).to(torch.bfloat16).to(DEV)
+    lse = torch.empty(Q.shape[:2], device=DEV)
+    O = api.pw_chunk_attn(Q, _dev(Kp), _dev(Vp), _i32(table), _i32(cu), _i32(cl), max_q_len=max(qlens), k_scale=S, v_scale=S, lse=lse)
+    torch.cuda.synchronize()
+    x = ref.f64(Q)
+    want, wl, bO, bl = ref.attn(x, Kp, Vp, table, qlens, ctx, S, S, 128 ** -0.5)
+    # what the small elements' error moves a score by, at most: each times the largest key in its dimension
+    k_most, v_most = np.nanmax(np.abs(ref.VALUES[Kp]), (0, 1, 2)) * S, np.nanmax(np.abs(ref.VALUES[Vp])) * S
+    top = np.abs(x).max(-1, keepdims=True)
+    e = (np.where(np.abs(x) < top * 2.0 ** -13, top * 2.0 ** -21, 0.0) * k_most).sum(-1) * 128 ** -0.5
+    # a score's error moves the log-sum-exp by as much at most, and the weights by twice that
+    ref.assert_bf16(O, want, bO + 2 * e[..., None] * v_most, "O")
+    assert (np.abs(ref.f64(lse) - wl) <= bl + e).all(), f"lse off by {np.abs(ref.f64(lse) - wl).max():.3g}"
