@@ -13,10 +13,12 @@
 // cycles with conversions and a store a code, 260 so.
 //
 // The running maximum of a row is a reference that only has to keep its weights in range: it lies
-// above the scores and moves when one exceeds it, to 4 (base 2) above that score, so that a row's
-// largest weight lies in [2^-4, 1] and the smallest step of f16 (2^-24, weights below 2^-14) is at most
-// 2^-20 of it.  That costs one vote per block instead of a reduction over the keys, which lie along
-// the threads here.
+// above the scores and moves when one exceeds it, to 2 (base 2) above that score, so that a row's
+// largest weight lies in [2^-2, 1] and a weight below f16's normal range (2^-14) is off by at most half of
+// its smallest step, 2^-25, or 2^-23 of the largest.  That costs one vote per block instead of a reduction over
+// the keys, which lie along the threads here.  Moves further up are fewer, and lose more: 4 above, a
+// row of 128k keys that together make 3% beside one key could lose all of them (decode 64 ragged / 4 x 128k /
+// verify 32 x 5: 4 above 205 / 179 / 95 us, 2 above 206 / 180 / 98, 1 above 208 / 181 / 101).
 //
 // Two CTAs share an SM, each with its own stretch of the work, so that one computes while the other
 // starts or ends a tile.  The two softmax warps that share a quarter of the keys share the rows: four of
@@ -53,7 +55,7 @@ constexpr int kJobs = 4;
 // Query tiles: S runs up to one block, so up to one tile, ahead of the products, and a tile's slot is
 // free when its results are written.
 constexpr int kQ = 2;
-constexpr float kAbove = 4.f;  // a row's reference moves to this much above its largest score (base 2)
+constexpr float kAbove = 2.f;  // a row's reference moves to this much above its largest score (base 2)
 
 template <int NT> constexpr int kStagesFor = NT == 16 ? 3 : 2;
 template <int NT> constexpr int kCols = (3 * NT + 15) / 16 * 16; // columns of the weights: a whole number of cores
@@ -334,6 +336,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
                         for (int i = 0; i < R8; ++i) {
                             const float4 al = *reinterpret_cast<const float4 *>(alpha + 8 * i);
+                            if (al.x * al.y * al.z * al.w == 1.f) // none of the four moves (a factor is 1 or at most 2^-kAbove)
+                                continue;
 #pragma unroll 1
                             for (int part = 0; part < 3; ++part) {
                                 const uint32_t at = o_addr + part * NT + 8 * i;

@@ -262,7 +262,9 @@ pw_status pw_chunk_workspace_size(int B, int64_t T, int Hq, int Hkv, int max_q_l
  * whole row, or, of a value that the whole tile sees, that dimension), and of no other; an infinity
  * or NaN in a query makes NaN of its own row.
  * Elements of a query within 2^13 of its row's largest enter the scores exactly, smaller ones with an error
- * of at most 2^-21 of the largest; scores are summed in fp32.
+ * of at most 2^-21 of the largest; scores are summed in fp32.  The row's sum of weights is taken in fp32.
+ * Into the product with V a weight enters rounded to f16: off by 2^-11 of itself at most, or by 2^-23 of the
+ * row's largest weight where that is more.
  * Results do not depend on timing: the same inputs give the same bits.
  * Supported: Hq % Hkv == 0, positions below 2^30, T * Hq < 2^31 - 4096, n_phys * Hkv * 64 < 2^31.
  * sm_scale is positive and finite, scales too.

@@ -1,5 +1,6 @@
 """pw_chunk_attn where the values are what can go wrong: NaN marks of short tiles, equal bits of repeated
-calls on ragged batches, queries with one large element (tokens_ref.py holds the plain 64-bit forms)."""
+calls on ragged batches, queries with one large element, small weights that count by their number alone
+(tokens_ref.py holds the plain 64-bit forms)."""
 import numpy as np
 import pytest
 import torch
@@ -109,3 +110,33 @@ def test_queries_with_one_large_element(qlens, ctx, octaves):
     # a score's error moves the log-sum-exp by as much at most, and the weights by twice that
     ref.assert_bf16(O, want, bO + 2 * e[..., None] * v_most, "O")
     assert (np.abs(ref.f64(lse) - wl) <= bl + e).all(), f"lse off by {np.abs(ref.f64(lse) - wl).max():.3g}"
+
+
+@pytest.mark.parametrize("q,B", [(1, 592), (2, 300), (32, 148)])
+def test_one_key_above_many(q, B):
+    """64k or 128k keys behind one that outweighs each of them by 2^17 to 2^24 and whose value is zero: the others'
+    small weights, which only their number makes count, are the output."""
+    rng = np.random.default_rng(3)
+    n, Hq = 131072, 8
+    if q > 16:
+        n = 65536
+    pages = n // 64
+    Kp, Vp = _codes(rng, (pages, 1, 64, 128)), _codes(rng, (pages, 1, 64, 128))
+    Vp[:] = 0x38 + Vp % 4  # 1 to 1.375, so that nothing cancels
+    Kp[..., 0] = 0
+    Kp[0, 0, 0] = 0
+    Kp[0, 0, 0, 0] = 0x78  # 256
+    Vp[0, 0, 0] = 0
+    gap = np.linspace(17, 24, Hq)  # octaves
+    x = np.where(np.arange(128) == 0, (gap * np.log(2) / 256)[:, None], 0.5 / (64 * 127 ** 0.5))[None] * np.ones((q, 1, 1))
+    Q = torch.from_numpy(x).to(torch.bfloat16)
+    table = np.broadcast_to(np.arange(pages, dtype=np.int32), (B, pages))  # all sequences read the same pages
+    cu, cl = ref.batch([q] * B, [n - q] * B)
+    O = api.pw_chunk_attn(Q.repeat(B, 1, 1).to(DEV), _dev(Kp), _dev(Vp), _i32(table), _i32(cu), _i32(cl), max_q_len=q, sm_scale=1.0)
+    torch.cuda.synchronize()
+    want, _, bO, _ = ref.attn(ref.f64(Q), Kp, Vp, table[:1], [q], [n - q], 1.0, 1.0, 1.0)
+    # A weight below f16's normal range is off by at most half of its smallest step, 2^-25, and a row's largest
+    # weight is at least 1/4 when it rounds: 2^-23 of it a key, of which 2^-25 is in the bound already.
+    bO = bO + n * 3 * 2.0 ** -25 * 1.375
+    for i in range(0, B, 37):
+        ref.assert_bf16(O[i * q:(i + 1) * q], want, bO, f"sequence {i}")
