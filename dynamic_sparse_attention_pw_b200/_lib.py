@@ -98,6 +98,10 @@ def binding():
         except ImportError as e:
             raise RuntimeError("_pw_binding.so is missing or does not load; build it with "
                                "`python -m dynamic_sparse_attention_pw_b200.build`") from e
+        from .build import binding_target
+        if _pw_binding.built_for != f"[built for {binding_target()}]":
+            raise RuntimeError(f"_pw_binding.so is {_pw_binding.built_for[1:-1]}, not for {binding_target()}; build it "
+                               "again with `python -m dynamic_sparse_attention_pw_b200.build`")
         _binding = _pw_binding
     return _binding
 

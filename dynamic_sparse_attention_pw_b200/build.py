@@ -3,6 +3,7 @@ argument marshalling for the calls that a decoding step makes) with g++ against 
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -53,15 +54,27 @@ def up_to_date() -> bool:
     return _newer(LIB, deps())
 
 
+def binding_target() -> str:
+    """What _pw_binding.so has to be compiled for: it uses torch's C++ classes and Python's C API."""
+    return f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pw.h")]):
+        return False
+    with open(BINDING, "rb") as f:
+        return f"[built for {binding_target()}]".encode() in f.read()
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pw.h")]):
+    if not force and _binding_up_to_date():
         return BINDING
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           *[f"-isystem{i}" for i in inc], BINDING_SRC, "-o", BINDING,
+           f'-DPW_BUILT_FOR="{binding_target()}"', *[f"-isystem{i}" for i in inc], BINDING_SRC, "-o", BINDING,
            "-L" + HERE, "-l:libpw.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
@@ -70,17 +83,20 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+def build(force: bool = False, verbose: bool = False, extra=(), binding: bool = True) -> str:
+    """libpw.so, and unless binding is False (a user of the C ABI alone needs neither g++ nor torch's headers)
+    the compiled part of its Python binding; what is up to date stays, unless force."""
     if force or not up_to_date():
         cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", LIB, *sources()]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
-    build_binding(verbose=verbose)
+    if binding:
+        build_binding(force=force, verbose=verbose)
     return LIB
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose=True,
+    build(force="--force" in sys.argv, verbose=True, binding="--no-binding" not in sys.argv,
           extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
     print(LIB)

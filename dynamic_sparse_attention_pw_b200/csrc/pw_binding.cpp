@@ -351,4 +351,18 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pw_binding", "Argument marshallin
 
 } // namespace
 
-PyMODINIT_FUNC PyInit__pw_binding(void) { return PyModule_Create(&module); }
+// What it was compiled for: build.py looks for the text in the file, the loader at the attribute.
+#ifndef PW_BUILT_FOR
+#error "PW_BUILT_FOR: the versions of torch and Python (build.py sets it)"
+#endif
+
+PyMODINIT_FUNC PyInit__pw_binding(void)
+{
+    static const char text[] = "[built for " PW_BUILT_FOR "]";
+    PyObject *const m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", text) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
