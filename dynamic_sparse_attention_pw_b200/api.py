@@ -255,8 +255,10 @@ def chunk_workspace(B: int, T: int, Hq: int, Hkv: int, max_q_len: int | None = N
                     device="cuda") -> torch.Tensor:
     """Scratch for pw_chunk_attn calls of these shapes, to be kept between them.  Calls that overlap
     in time (two streams) need one each."""
+    if max_q_len is None:
+        max_q_len = max(T, 1)
     n = C.c_size_t()
-    _check(_lib.load().pw_chunk_workspace_size(B, T, Hq, Hkv, max_q_len or max(T, 1), C.byref(n)),
+    _check(_lib.load().pw_chunk_workspace_size(B, T, Hq, Hkv, max_q_len, C.byref(n)),
            "pw_chunk_workspace_size")
     return torch.empty(n.value, dtype=torch.uint8, device=device)
 
