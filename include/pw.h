@@ -223,8 +223,9 @@ pw_status pw_qk_norm_rope(const void *Q, int64_t q_stride_t, int64_t q_stride_h,
                           void *stream);
 
 /* Keys and values of the new tokens into the paged cache, with the keys' norm and rotation (as in
- * pw_qk_norm_rope) on the way.  The codes are E4M3 of key / k_scale and value / v_scale, rounded
- * to nearest even; magnitudes above 448 become 448, NaN stays NaN.  The row of position p goes to
+ * pw_qk_norm_rope) on the way.  The codes are E4M3 of key and value times the reciprocal of their scale
+ * (rounded to fp32; for a power of two that is the quotient, for another scale a quotient next to a rounding
+ * border may go to either side of it), rounded to nearest even; magnitudes above 448 become 448, NaN stays NaN.  The row of position p goes to
  * slot p % 64 of physical page page_table[b * max_pages + p / 64]; nothing else of the cache is
  * written.  Two tokens of one call must not share a slot.
  *   K, V              bf16 rows of heads, Hkv heads each
