@@ -298,9 +298,10 @@ def pw_chunk_attn(Q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
 def extend(Q, K, V, K_pages, V_pages, page_table, cu_seqlens, ctx_lens=None, max_q_len=None,
            q_weight=None, k_weight=None, eps: float = 1e-6, rope=None, interleaved: bool = False,
            k_scale: float = 1.0, v_scale: float = 1.0, sm_scale=None, window: int = 0,
-           workspace=None, status=None, stream=None) -> torch.Tensor:
+           workspace=None, status=None, stream=None, O=None, lse=None) -> torch.Tensor:
     """One complete step of new tokens: queries normalised and rotated, keys and values appended to
-    the cache, and the new tokens' attention over it, on one stream.  Returns O bf16 [T, Hq, 128]."""
+    the cache, and the new tokens' attention over it, on one stream.  O and lse as in pw_chunk_attn.
+    Returns O bf16 [T, Hq, 128]."""
     Qn, _ = pw_qk_norm_rope(Q, None, cu_seqlens, ctx_lens, q_weight=q_weight, eps=eps, rope=rope,
                             interleaved=interleaved, status=status, stream=stream)
     pw_append(K, V, K_pages, V_pages, page_table, cu_seqlens, ctx_lens, k_scale=k_scale,
@@ -308,7 +309,8 @@ def extend(Q, K, V, K_pages, V_pages, page_table, cu_seqlens, ctx_lens=None, max
               status=status, stream=stream)
     return pw_chunk_attn(Qn, K_pages, V_pages, page_table, cu_seqlens, ctx_lens,
                          max_q_len=max_q_len, k_scale=k_scale, v_scale=v_scale, sm_scale=sm_scale,
-                         window=window, workspace=workspace, status=status, stream=stream)
+                         window=window, O=O, lse=lse, workspace=workspace, status=status,
+                         stream=stream)
 
 
 def device_inputs(inp: dict, device="cuda") -> dict:

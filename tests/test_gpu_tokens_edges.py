@@ -1,4 +1,4 @@
-"""pw_append on the GPU: codes under scales that are no power of two
+"""pw_append and extend on the GPU: codes under scales that are no power of two, extend's outputs
 (tokens_ref.py holds the plain 64-bit forms)."""
 import numpy as np
 import pytest
@@ -45,3 +45,35 @@ def test_append_codes_are_of_the_product_with_the_reciprocal(scale):
         assert np.array_equal(codes, want)
         quotient = ref.f64(x) / np.float64(s32)
         ref.assert_e4m3(codes, quotient, 2 * ref.U32 * np.abs(quotient))  # the reciprocal's rounding and the product's
+
+
+@pytest.mark.parametrize("qlens,ctx", [([1, 1, 1], [0, 62, 300]), ([70, 5], [100, 0])])
+def test_extend_into_the_callers_outputs(qlens, ctx):
+    """O and lse of the caller are what the single calls give, and rows behind the last sequence stay."""
+    rng = np.random.default_rng(31)
+    Hq, Hkv, pad = 8, 2, 3
+    cu, cl = ref.batch(qlens, ctx)
+    T = int(cu[-1])
+    table, n_phys = ref.pages_for(qlens, ctx, rng)
+    codes = torch.from_numpy(rng.standard_normal((2, n_phys, Hkv, 64, 128)) * 64).to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+    qkv = _bf16(rng, T + pad, Hq + 2 * Hkv, 128)
+    Q, K, V = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    wq, wk, rope = _bf16(rng, 128), _bf16(rng, 128), api.rope_table(400, device=DEV)
+    status = api.new_status(DEV)
+    dev = (_i32(table), _i32(cu), _i32(cl))
+    scales = dict(k_scale=2.0 ** -6, v_scale=2.0 ** -6)
+
+    one = codes.clone()
+    O = torch.full((T + pad, Hq, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T + pad, Hq), 7.0, device=DEV)
+    got = api.extend(Q, K, V, one[0], one[1], *dev, max_q_len=max(qlens), q_weight=wq, k_weight=wk, rope=rope, status=status, O=O,
+                     lse=lse, **scales)
+    two = codes.clone()
+    Qn, _ = api.pw_qk_norm_rope(Q, None, *dev[1:], q_weight=wq, rope=rope)
+    api.pw_append(K, V, two[0], two[1], *dev, k_weight=wk, rope=rope, status=status, **scales)
+    lse2 = torch.empty_like(lse)
+    want = api.pw_chunk_attn(Qn, two[0], two[1], *dev, max_q_len=max(qlens), lse=lse2, status=status, **scales)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and got is O
+    assert torch.equal(one, two) and torch.equal(O[:T], want[:T]) and torch.equal(lse[:T], lse2[:T])
+    assert bool((O[T:] == 7.0).all()) and bool((lse[T:] == 7.0).all())
