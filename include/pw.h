@@ -267,6 +267,8 @@ pw_status pw_chunk_workspace_size(int B, int64_t T, int Hq, int Hkv, int max_q_l
  * Into the product with V a weight enters rounded to f16: off by 2^-11 of itself at most, or by 2^-23 of the
  * row's largest weight where that is more.
  * Results do not depend on timing: the same inputs give the same bits.
+ * Scores times log2 e stay below 2^24 in magnitude; a row with larger ones may come out NaN.
+ * O, lse and the workspace overlap no other argument.
  * Supported: Hq % Hkv == 0, positions below 2^30, T * Hq < 2^31 - 4096, n_phys * Hkv * 64 < 2^31.
  * sm_scale is positive and finite, scales too.
  * A page-table entry outside [0, n_phys), or a position outside the table's row, records

@@ -1,6 +1,6 @@
 """pw_chunk_attn where the values are what can go wrong: NaN marks of short tiles, equal bits of repeated
-calls on ragged batches, queries with one large element, small weights that count by their number alone
-(tokens_ref.py holds the plain 64-bit forms)."""
+calls on ragged batches, queries with one large element, small weights that count by their number alone,
+large scores (tokens_ref.py holds the plain 64-bit forms)."""
 import numpy as np
 import pytest
 import torch
@@ -140,3 +140,22 @@ def test_one_key_above_many(q, B):
     bO = bO + n * 3 * 2.0 ** -25 * 1.375
     for i in range(0, B, 37):
         ref.assert_bf16(O[i * q:(i + 1) * q], want, bO, f"sequence {i}")
+
+
+@pytest.mark.parametrize("qlens,ctx", [([1], [900]), ([5], [900]), ([200], [900])])
+def test_scores_up_to_the_stated_limit(qlens, ctx):
+    """Scores of up to 2^23 (base 2): a row is little but its largest key, and finite.  The scores themselves are
+    off by at most 2^-20 of sum |q k|, and so is the log-sum-exp."""
+    rng = np.random.default_rng(4)
+    cu, cl = ref.batch(qlens, ctx)
+    table, n_phys = ref.pages_for(qlens, ctx, rng)
+    Kp, Vp = _codes(rng, (n_phys, 2, 64, 128)), _codes(rng, (n_phys, 2, 64, 128))
+    Q = torch.from_numpy(rng.standard_normal((cu[-1], 8, 128)) * 1500).to(torch.bfloat16).to(DEV)
+    lse = torch.empty(Q.shape[:2], device=DEV)
+    O = api.pw_chunk_attn(Q, _dev(Kp), _dev(Vp), _i32(table), _i32(cu), _i32(cl), max_q_len=max(qlens), sm_scale=1.0, v_scale=S, lse=lse)
+    torch.cuda.synchronize()
+    want, wl, _, bl = ref.attn(ref.f64(Q), Kp, Vp, table, qlens, ctx, 1.0, S, 1.0)
+    assert 2.0 ** 22 < np.abs(wl).max() * 1.4427 < 2.0 ** 24
+    assert (np.abs(ref.f64(lse) - wl) <= bl).all()
+    top = np.abs(ref.VALUES[Vp]).max() * S
+    assert bool((O.abs() <= top * (1 + 2.0 ** -8) * (1 + 2.0 ** -10)).all())  # an average of values; weights and output are rounded
