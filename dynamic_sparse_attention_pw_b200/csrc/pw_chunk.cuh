@@ -524,7 +524,7 @@ size_t tiles_workspace();
 
 // Joins the partial results of the tiles that were cut: block j does the tile that stretch j starts
 // inside of, unless an earlier stretch starts inside of it too.  A warp has NT / 64 rows (one of a
-// small tile).  Where the attention kernel leaves registers (few rows), the blocks are brought up while
+// small tile).  Behind the kernel for few rows, which leaves registers, the blocks are brought up while
 // it still runs (programmatic launch) and wait for its end: 128 threads of 64 registers fit beside it.
 template <int NT>
 __global__ void __launch_bounds__(128, 8) k_chunk_merge(const ChunkLaunch L)
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(128, 8) k_chunk_merge(const ChunkLaunch L)
     }
 }
 
-// Lets k_chunk_merge come up; every thread of the attention kernels calls it.
+// Lets k_chunk_merge come up; every thread of the kernel for few rows calls it.
 __device__ __forceinline__ void allow_merge() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // CTAs of the attention kernel on a device of that many SMs; sets what divides by it.
@@ -628,7 +628,7 @@ cudaError_t merge_launch(const ChunkLaunch &L, int ctas, cudaStream_t st)
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cfg.attrs = &early;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = NT <= 32 ? 1 : 0; // the kernel for many rows leaves it no registers
     return cudaLaunchKernelEx(&cfg, k_chunk_merge<NT>, L);
 }
 
