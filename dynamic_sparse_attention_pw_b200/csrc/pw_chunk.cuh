@@ -36,38 +36,6 @@ __host__ __device__ constexpr int max_ctas() { return NT <= 32 ? 2 * kSms : kSms
 constexpr int kBlock = 128;    // keys per block
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
 
-using F2 = uint64_t; // two fp32, for the packed instructions
-
-__device__ __forceinline__ F2 pack2(float lo, float hi)
-{
-    F2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-
-__device__ __forceinline__ void unpack2(F2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-
-__device__ __forceinline__ F2 add2(F2 a, F2 b)
-{
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // What the tiles of a call depend on besides their sequence.
 struct Shape {
     int G, window, last; // last position a page table's row can hold

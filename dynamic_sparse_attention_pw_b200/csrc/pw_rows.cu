@@ -31,31 +31,6 @@ using namespace tokens;
 
 constexpr int kWarps = 4;
 
-using F2 = uint64_t; // two fp32, for the packed instructions
-
-__device__ __forceinline__ F2 pack2(float lo, float hi)
-{
-    F2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-
-__device__ __forceinline__ void unpack2(F2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 __device__ __forceinline__ F2 swap2(F2 v)
 {
     float lo, hi;
