@@ -52,8 +52,8 @@ cudaError_t page_tensor(const uint8_t *pages, const ChunkLaunch &L, CUtensorMap 
 namespace {
 
 // Rows of the longest chunk that share a kv head, up to which the kernel for few rows is taken: one of
-// its tiles.  (32 users of 4k keys, 4 heads a group: chunks of 8 tokens 96 us against 121 us with the
-// large tiles, of 12 tokens 150 us against 123 us; 4 users of 8k: 45 against 49 us, 57 against 51 us.)
+// its tiles.  (32 users of 4k keys, 4 heads a group: chunks of 8 tokens 100 us against 121 us with the
+// large tiles, of 12 tokens 150 us against 123 us; 4 users of 8k: 49 us either way, 57 against 51 us.)
 constexpr int64_t kFewRows = 32;
 
 int64_t rows_of(int Hq, int Hkv, int max_q_len) { return static_cast<int64_t>(max_q_len) * (Hq / Hkv); }

@@ -32,11 +32,10 @@
 //   warp 10      the next tile's queries
 //
 // What bounds it: the bytes of the cache.  64 sequences of 500 to 16k tokens, 8 query heads a kv head
-// (1.1 GB): 191 to 205 us (B200s differ), 5.4 to 5.8 TB/s with launch and merge; four of 128k: 172 to
-// 181 us, 5.9 to 6.25 TB/s (a copy: 6.55).  With 20 rows (5 drafted tokens, 4 heads) the weights'
-// arithmetic takes longer than the bytes: 32 sequences of 1k to 8k 96 us, 3.2 TB/s (tiles of 32 rows
-// for them: 105 us).  Small calls are
-// latency: 13.9 us for one token over 2k keys.
+// (1.1 GB): 196 to 207 us (B200s differ), 5.4 to 5.6 TB/s with launch and merge; four of 128k: 174 to
+// 182 us, 5.9 to 6.2 TB/s (a copy: 6.55).  With 20 rows (5 drafted tokens, 4 heads) the weights'
+// arithmetic takes longer than the bytes: 32 sequences of 1k to 8k 96 to 98 us, 3.1 TB/s (tiles of 32 rows
+// for them: 105 us).  Small calls are latency: 16.4 us for one token over 2k keys.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>

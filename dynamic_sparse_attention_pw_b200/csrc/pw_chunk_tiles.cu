@@ -10,7 +10,15 @@
 //
 // A row's running maximum is a reference, a whole number, that moves when a score of a chunk of 32
 // keys exceeds it by more than 2^15 (f16 ends at 2^16); what the row has so far, the weights of the
-// block's earlier chunks among it, is then scaled by a power of two.
+// block's earlier chunks among it, is then scaled by a power of two.  It lies less than 1 above the row's largest
+// score when it moves, so that the largest weight is more than 1/2 and a weight below f16's normal range is off by
+// at most 2^-24 of it.  (Whole numbers below the score would halve that, and measured 203 us against 196 on
+// ragged chunks.)
+//
+// Weights enter P V as one f16, 2^-11 of themselves off at most, where pw_attn carries a second f16 with the rest:
+// from the 64-bit result, outputs differ by 1.68e-3 rel-L2, of which bf16's rounding alone makes 1.66e-3
+// (rounded to bf16, the two differ by up to 9.7e-4).  The second products would take the tensor cores from
+// 2400 to 3540 of a block's 3500 cycles: 2.41 ms where 1.89 are taken (2048 tokens at 32k).
 //
 //   warps 0-3    softmax, first half; the end of its rows
 //   warps 4-7    softmax, second half
@@ -19,8 +27,8 @@
 //   warp 13      the products
 // What bounds it: the chain of a half's block -- softmax 1650 to 2050 cycles, wake-up 350, P V 570, S 600,
 // S back to the softmax 240 -- of which the other half's hides most: a block of 256 rows takes 3500
-// cycles, the tensor cores' share of it 2400.  2048 tokens at 32k (2.13 TFLOP): 1.63 ms from a cold cache,
-// 1.88 ms in a row under the power limit.  Tried and slower: a product warp for each half (the halves
+// cycles, the tensor cores' share of it 2400.  2048 tokens at 32k (2.13 TFLOP): 1.88 to 1.93 ms a call
+// in a row, under the power limit (1.64 ms with a pause and a flushed L2 before each).  Tried and slower: a product warp for each half (the halves
 // fall into step: 2.14 ms against 1.73), steps of 64 keys with S a step ahead (M = 128, N = 64 products
 // take as long as N = 128: 2.48), two threads a row (1.79), part of the exponentials on the
 // multiply-add units (a quarter of them 1.86), waits that spin (1.79).

@@ -13,10 +13,10 @@
 // on packed fp32 pairs.  (A first form that applied weight and rotation row by row was bound by its
 // instructions, 71% of the issue slots at 67% of the memory rate.)  How many heads a warp takes is a
 // matter of filling the GPU: few tokens, one group of four heads each; many, up to kMost groups.
-// A prompt of 16k tokens, 64 + 8 heads (0.6 GB): 108 us, 5.65 TB/s; sixteen groups a warp 113 us where two
-// took 180 us.  Append of two such prompts (8 + 8 heads, 0.2 GB): 49 us, 55 from a cold cache (61 with the
-// keys' factors formed before the values went out); its warps have only four groups, and the chain
-// position, page, table row before the first store bounds them.
+// A prompt of 16k tokens, 64 + 8 heads (0.6 GB): 106 to 109 us, 5.6 TB/s; sixteen groups a warp 113 us where two
+// took 180 us.  Append of two such prompts (8 + 8 heads, 0.2 GB): 49 us (the values go out before the keys'
+// factors are formed); its warps have only four groups, and the chain position, page, table row before the
+// first store bounds them.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>

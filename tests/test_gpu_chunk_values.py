@@ -7,6 +7,7 @@ import torch
 
 from dynamic_sparse_attention_pw_b200 import api
 
+import parity
 import tokens_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -159,3 +160,23 @@ def test_scores_up_to_the_stated_limit(qlens, ctx):
     assert (np.abs(ref.f64(lse) - wl) <= bl).all()
     top = np.abs(ref.VALUES[Vp]).max() * S
     assert bool((O.abs() <= top * (1 + 2.0 ** -8) * (1 + 2.0 ** -10)).all())  # an average of values; weights and output are rounded
+
+
+@pytest.mark.parametrize("qlens,ctx,Hq,Hkv", [
+    ([1] * 24, [90 * i for i in range(24)], 64, 8),        # tiles of 16 rows
+    ([5] * 6, [100, 2000, 700, 0, 5000, 64], 32, 8),       # 24
+    ([4] * 6, [100, 2000, 700, 0, 5000, 64], 64, 8),       # 32
+    ([300, 40, 1], [2000, 0, 900], 32, 8),                 # large ones
+])
+def test_outputs_within_the_bar_of_the_sparse_attention(qlens, ctx, Hq, Hkv):
+    """Max-abs 2e-2 and rel-L2 1e-3 of the 64-bit result rounded to bf16: the bar that pw_attn is held to."""
+    rng = np.random.default_rng(5)
+    cu, cl = ref.batch(qlens, ctx)
+    table, n_phys = ref.pages_for(qlens, ctx, rng)
+    Kp, Vp = _codes(rng, (n_phys, Hkv, 64, 128)), _codes(rng, (n_phys, Hkv, 64, 128))
+    Q = torch.from_numpy(rng.standard_normal((cu[-1], Hq, 128)) * np.linspace(0.5, 3.0, Hq)[:, None]).to(torch.bfloat16).to(DEV)
+    O = api.pw_chunk_attn(Q, _dev(Kp), _dev(Vp), _i32(table), _i32(cu), _i32(cl), max_q_len=max(qlens), k_scale=S, v_scale=S)
+    torch.cuda.synchronize()
+    want = ref.attn(ref.f64(Q), Kp, Vp, table, qlens, ctx, S, S, 128 ** -0.5)[0]
+    got = O.view(torch.int16).cpu().numpy().view(np.uint16)
+    parity.compare_rows(got.reshape(-1, 128), want.reshape(-1, 128), "pw_chunk_attn")
